@@ -197,6 +197,131 @@ int mx_gemm_mx(const void* a_q, const uint8_t* a_s, int32_t a_fmt, const void* b
                const uint8_t* b_s, int32_t b_fmt, int64_t M, int64_t N, int64_t K,
                int32_t c_fmt, void* c_q, uint8_t* c_s, mx_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Decoder-layer operators around the GEMM: the norm in front of it, products of
+ * a few tokens, the key/value cache and attention over it.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * mx_rmsnorm_quantize -- root-mean-square norm of h = x + r with an MX output, one
+ * pass over the rows:
+ *   h = x + r, rounded to the source type (h = x where r is NULL)
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps)
+ *   y = h * rstd * w, in fp32
+ *   q_row, s_row: y quantized as mx_quantize does it (row layout, MX_RNE).
+ *   x, r    [rows x cols] of type src, leading dimensions ld_x, ld_r; r may be
+ *           NULL (no residual).  w [cols] of type src.
+ *   eps     >= 0.
+ *   h, y    [rows x cols] of type src, leading dimensions ld_h, ld_y; NULL: not
+ *           written.  y is rounded to nearest even; the codes come from the fp32
+ *           y.  h may be x or r (same pointer and leading dimension).
+ *   q_row, s_row  any format, row layout of mx_quantize.
+ *   rstd    [rows] fp32, for mx_rmsnorm_backward; NULL: not written.
+ * Pointers to rows, w and q_row 16-byte aligned, leading dimensions multiples of
+ * 16 bytes.  Any rows < 2^31 and cols <= 2^24.  A row whose mean square is not
+ * finite gives what the formulas give.
+ */
+int mx_rmsnorm_quantize(const void* x, int64_t ld_x, const void* r, int64_t ld_r, const void* w, int64_t rows,
+                        int64_t cols, int32_t src, int32_t fmt, float eps, void* h, int64_t ld_h, void* y,
+                        int64_t ld_y, void* q_row, uint8_t* s_row, float* rstd, mx_stream_t stream);
+
+/*
+ * mx_rmsnorm_backward -- gradients of the norm for the gradient dy of y (the
+ * rounding to MX passes it on unchanged).  With xhat = h * rstd and g = dy * w:
+ *   dx = rstd * (g - xhat * mean over the row of (g * xhat)) + dh
+ *   dw = sum over rows of dy * xhat
+ * dx is the gradient of h, and so of x and of r alike.
+ *   dy, h   [rows x cols] of type src;  rstd [rows] as the forward wrote it.
+ *   dh      the gradient that reaches h another way (the residual stream), or NULL.
+ *   dx      [rows x cols] of type src; may be dy or dh.
+ *   dw      [cols] fp32, overwritten; its sums are taken in a fixed order.
+ *   workspace  mx_rmsnorm_backward_workspace(rows, cols, src) bytes, 16-byte
+ *           aligned, in use until the call's work is done.  MX_ERR_SHAPE if smaller.
+ * Alignment and sizes as for mx_rmsnorm_quantize.  rows == 0 writes zeros to dw.
+ */
+int mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* w,
+                        const float* rstd, const void* dh, int64_t ld_dh, int64_t rows, int64_t cols,
+                        int32_t src, void* dx, int64_t ld_dx, float* dw, void* workspace,
+                        int64_t workspace_bytes, mx_stream_t stream);
+int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int32_t src);
+
+/*
+ * mx_gemv -- y = x * W^T for a few tokens x in bf16 and weights W in 4-bit MX:
+ *   y[m, n] = sum over blocks kb of 2^(s[n, kb] - 127) * sum_{k in kb} x[m, k] * P[n, k].
+ *   x       [M x K] bf16, leading dimension ld_x >= K, no alignment beyond 2 bytes.
+ *   w_q, w_s  W as [N x K] row-wise MX, what mx_quantize writes for it; w_q 16-byte
+ *           aligned.
+ *   w_fmt   MX_E2M1 (other formats: MX_ERR_UNSUPPORTED).
+ *   y       [M x N] fp32, leading dimension ld_y >= N.
+ * A weight times its scale is exact in bf16 (for scale codes >= 1), so products are
+ * exact and summed in fp32.  Made for M up to 32, where reading the weights is the
+ * work: larger M is computed 32 tokens at a time, and mx_gemm is faster there.
+ */
+int mx_gemv(const void* x, int64_t ld_x, const void* w_q, const uint8_t* w_s, int32_t w_fmt, int64_t M, int64_t N,
+            int64_t K, float* y, int64_t ld_y, mx_stream_t stream);
+/* mx_gemv_bf16 -- the same with y in bf16, rounded to nearest even. */
+int mx_gemv_bf16(const void* x, int64_t ld_x, const void* w_q, const uint8_t* w_s, int32_t w_fmt, int64_t M,
+                 int64_t N, int64_t K, uint16_t* y, int64_t ld_y, mx_stream_t stream);
+
+/*
+ * A paged key/value cache in 8-bit MX.  Keys and values are each `pages` pages of
+ * `page` tokens: elements [pages][heads][page][dim] in fmt, scales
+ * [pages][heads][page][dim / 32].  A block is 32 consecutive values of one token's
+ * head.  fmt MX_E4M3 or MX_E5M2; dim 64, 128 or 256; page a multiple of 16; all
+ * four arrays 16-byte aligned (others: MX_ERR_UNSUPPORTED, MX_ERR_ALIGN).
+ */
+typedef struct {
+  void* k_q;
+  uint8_t* k_s;
+  void* v_q;
+  uint8_t* v_s;
+  int64_t pages;
+  int32_t heads, page, dim, fmt;
+} mx_cache;
+
+/*
+ * mx_cache_write -- quantizes the keys and values of `tokens` tokens as mx_quantize
+ * does (MX_RNE, blocks along dim) into the slots of a cache.
+ *   k, v    [tokens][heads][dim] of type src: element (t, h, d) at t * ld + h * hs + d.
+ *           16-byte aligned, ld and hs multiples of 16 bytes.
+ *   slots   [tokens] device array: token t goes to place slot % page of page
+ *           slot / page.  A slot outside [0, pages * page) is not written.  Slots of
+ *           one call are different.
+ */
+int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t hs_k, const void* v, int64_t ld_v,
+                   int64_t hs_v, int32_t src, int64_t tokens, const int64_t* slots, mx_stream_t stream);
+
+/*
+ * mx_attention -- softmax attention of Lq query tokens of each of B requests over
+ * the tokens of a cache.  Query i of request b sees the tokens
+ * t < lens[b] - Lq + i + 1: the queries are the request's last tokens, whose keys
+ * and values have been written.  Query heads share key/value heads in groups of
+ * heads_q / heads.
+ *   q       [B * Lq][heads_q][dim] bf16, ld_q elements between tokens, 16-byte
+ *           aligned rows.
+ *   table   [B][ld_table] device array: token t of request b lies in page
+ *           table[b][t / page].  Entries outside [0, pages) hold no tokens.
+ *   lens    [B] device array, tokens cached of each request, the queries' own
+ *           included; clamped to [0, max_len].
+ *   scale   factor of the scores (1 / sqrt(dim) as a rule).
+ *   max_len host-known bound of lens, at most ld_table * page (MX_ERR_SHAPE).  The
+ *           split of the work depends on it.
+ *   o       [B * Lq][heads_q][dim] bf16, ld_o elements between tokens.
+ *   lse     [B * Lq][heads_q] fp32, log of the sum of exp(scores); may be NULL.
+ *   workspace  mx_attention_workspace(...) bytes (may be 0), 16-byte aligned, in
+ *           use until the call's work is done.  MX_ERR_SHAPE if smaller.
+ * A query that sees no token gets o = 0 and lse = -inf.  What the cache holds
+ * beyond a query's tokens, NaN included, does not reach it.  Scores, sums and
+ * outputs are held in fp32; the weights p are rounded to bf16 for the second
+ * product.
+ */
+int mx_attention(const mx_cache* cache, const void* q, int64_t ld_q, const int32_t* table, int64_t ld_table,
+                 const int32_t* lens, int64_t B, int64_t Lq, int64_t heads_q, float scale, int64_t max_len,
+                 uint16_t* o, int64_t ld_o, float* lse, void* workspace, int64_t workspace_bytes,
+                 mx_stream_t stream);
+int64_t mx_attention_workspace(int64_t B, int64_t Lq, int64_t heads_q, int64_t heads, int64_t dim,
+                               int64_t max_len);
+
 /* Host-only helpers: bytes of a packed [rows x cols] element array (blocks
  * along cols, a short last block padded to 32 elements) and of its scale
  * array; -1 on a bad argument. */

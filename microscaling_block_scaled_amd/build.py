@@ -24,7 +24,8 @@ OBJ = os.path.join(PKG, "_build")
 GEN = os.path.join(OBJ, "gen")
 LIB = os.path.join(PKG, "libmx.so")
 
-SOURCES = ["mx_quant.hip", "mx_dequant.hip", "mx_gemm.hip", "mx_api.cpp"]
+SOURCES = ["mx_norm.hip", "mx_attention.hip", "mx_gemv.hip", "mx_quant.hip", "mx_dequant.hip", "mx_gemm.hip",
+           "mx_api.cpp", "mx_layer_api.cpp"]
 FORMATS = ["E4M3", "E5M2", "E2M3", "E3M2", "E2M1"]
 # every float pair, and MXINT8 with itself
 PAIRS = [(a, b) for a in FORMATS for b in FORMATS] + [("INT8", "INT8")]
@@ -78,7 +79,7 @@ def build(jobs: int | None = None, incremental: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES] + _gen_units()
     # the longest units first
-    srcs.sort(key=lambda s: (0 if "gemm_" in os.path.basename(s) else 1))
+    srcs.sort(key=lambda s: (0 if "gemm_" in os.path.basename(s) or "norm" in s else 1))
     newest = _newest_source()
     jobs = jobs or int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))
     with cf.ThreadPoolExecutor(max(1, min(jobs, len(srcs)))) as ex:

@@ -32,6 +32,12 @@ class QuantParams(ctypes.Structure):
                 ("counter_offset", ctypes.c_uint64)]
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [("k_q", ctypes.c_void_p), ("k_s", ctypes.c_void_p), ("v_q", ctypes.c_void_p),
+                ("v_s", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("dim", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
 class MXError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_str(status)} ({status})")
@@ -53,6 +59,23 @@ def _load():
     lib.mx_gemm_bf16.argtypes = [P, P, i32, P, P, i32, i64, i64, i64, P, i64, P]
     lib.mx_gemm_mx.restype = ctypes.c_int
     lib.mx_gemm_mx.argtypes = [P, P, i32, P, P, i32, i64, i64, i64, i32, P, P, P]
+    f32 = ctypes.c_float
+    lib.mx_rmsnorm_quantize.restype = ctypes.c_int
+    lib.mx_rmsnorm_quantize.argtypes = [P, i64, P, i64, P, i64, i64, i32, i32, f32, P, i64, P, i64, P, P, P, P]
+    lib.mx_rmsnorm_backward.restype = ctypes.c_int
+    lib.mx_rmsnorm_backward.argtypes = [P, i64, P, i64, P, P, P, i64, i64, i64, i32, P, i64, P, P, i64, P]
+    lib.mx_rmsnorm_backward_workspace.restype = i64
+    lib.mx_rmsnorm_backward_workspace.argtypes = [i64, i64, i32]
+    for gemv_ in (lib.mx_gemv, lib.mx_gemv_bf16):
+        gemv_.restype = ctypes.c_int
+        gemv_.argtypes = [P, i64, P, P, i32, i64, i64, i64, P, i64, P]
+    lib.mx_cache_write.restype = ctypes.c_int
+    lib.mx_cache_write.argtypes = [ctypes.POINTER(Cache), P, i64, i64, P, i64, i64, i32, i64, P, P]
+    lib.mx_attention.restype = ctypes.c_int
+    lib.mx_attention.argtypes = [ctypes.POINTER(Cache), P, i64, P, i64, P, i64, i64, i64, f32, i64, P, i64, P, P,
+                                 i64, P]
+    lib.mx_attention_workspace.restype = i64
+    lib.mx_attention_workspace.argtypes = [i64] * 6
     lib.mx_packed_bytes.restype = i64
     lib.mx_packed_bytes.argtypes = [i32, i64, i64]
     lib.mx_scale_bytes.restype = i64
@@ -68,7 +91,8 @@ lib = _load()
 
 # every symbol include/mx.h declares
 EXPORTS = ("mx_quantize", "mx_dequantize", "mx_gemm", "mx_gemm_bf16", "mx_gemm_mx",
-           "mx_packed_bytes", "mx_scale_bytes", "mx_status_str", "mx_version")
+           "mx_rmsnorm_quantize", "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace", "mx_gemv",
+           "mx_gemv_bf16", "mx_cache_write", "mx_attention", "mx_attention_workspace", "mx_packed_bytes", "mx_scale_bytes", "mx_status_str", "mx_version")
 
 
 def status_str(status: int) -> str:
@@ -182,4 +206,246 @@ def gemm_mx(a_q: torch.Tensor, a_s: torch.Tensor, a_fmt: int, b_q: torch.Tensor,
     _check(lib.mx_gemm_mx(_ptr(a_q), _ptr(a_s), a_fmt, _ptr(b_q), _ptr(b_s), b_fmt, M, N, K,
                           c_fmt, _ptr(o["q_row"]), _ptr(o["s_row"]), _stream(stream)),
            "mx_gemm_mx")
+    return o
+
+
+# ---------------------------------------------------------------------------
+# decoder-layer operators
+# ---------------------------------------------------------------------------
+_SRC = {torch.float32: SRC_F32, torch.bfloat16: SRC_BF16}
+
+
+def _on(stream, device):
+    """The HIP stream handle of a call, whose tensors must lie on the current device."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {device}")
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor whose memory belongs to the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new_rows(rows, cols, dtype, device, stream):
+    """A new [rows, cols] tensor whose rows start on 16 bytes."""
+    per = 8 if dtype == torch.bfloat16 else 4
+    pitch = -(-cols // per) * per
+    t = _empty((rows, pitch), dtype, device, stream)
+    return t if pitch == cols else t[:, :cols]
+
+
+def _rows(t, like, what):
+    """Checks a row-major matrix against another one; its address and pitch."""
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{what} must be {tuple(like.shape)} {like.dtype} on {like.device}")
+    st = t.stride()
+    if st[1] != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return t.data_ptr(), _pitch(t, st)
+
+
+def _pitch(t, st):
+    # the pitch of a single row says nothing: any that is allowed will do
+    return st[0] if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _vector(t, n, dtype, device, what):
+    if t.shape != (n,) or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} on {device}")
+    return t.data_ptr()
+
+
+def _out(t, shape, dtype, device, what):
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {shape} {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
+def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, fmt: int, eps: float = 1e-5,
+                     residual: torch.Tensor | None = None, want_y: bool = False,
+                     out: dict | None = None, stream=None) -> dict:
+    """Root-mean-square norm of h = x + residual (fp32 or bf16 rows) times w,
+    quantized row-wise to MX.  Returns q_row and s_row as ``quantize`` does, rstd
+    [rows] fp32, h where a residual is given, and y in x's type where ``want_y``
+    is set; ``out`` may supply any of them preallocated (h may be x or the
+    residual)."""
+    if x.dim() != 2 or x.dtype not in _SRC:
+        raise ValueError("x must be a 2-D fp32/bf16 CUDA tensor")
+    handle, dev = _on(stream, x.device), x.device
+    rows, cols = x.shape
+    px, ld_x = _rows(x, x, "x")
+    pr, ld_r = (None, 0) if residual is None else _rows(residual, x, "residual")
+    pw = _vector(w, cols, x.dtype, dev, "w")
+    o = dict(out or {})
+    packed, nblk = packed_bytes(fmt, 1, cols), (cols + 31) // 32
+    if "q_row" not in o:
+        o["q_row"] = _empty((rows, packed), torch.uint8, dev, stream)
+    if "s_row" not in o:
+        o["s_row"] = _empty((rows, nblk), torch.uint8, dev, stream)
+    if "rstd" not in o:
+        o["rstd"] = _empty((rows,), torch.float32, dev, stream)
+    if residual is not None and "h" not in o:
+        o["h"] = _new_rows(rows, cols, x.dtype, dev, stream)
+    if want_y and "y" not in o:
+        o["y"] = _new_rows(rows, cols, x.dtype, dev, stream)
+    ph, ld_h = _rows(o["h"], x, "h") if "h" in o else (None, 0)
+    py, ld_y = _rows(o["y"], x, "y") if "y" in o else (None, 0)
+    _check(lib.mx_rmsnorm_quantize(px, ld_x, pr, ld_r, pw, rows, cols, _SRC[x.dtype], fmt, eps, ph, ld_h, py, ld_y,
+                                   _out(o["q_row"], (rows, packed), torch.uint8, dev, "q_row"),
+                                   _out(o["s_row"], (rows, nblk), torch.uint8, dev, "s_row"),
+                                   _vector(o["rstd"], rows, torch.float32, dev, "rstd"), handle),
+           "mx_rmsnorm_quantize")
+    return o
+
+
+def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor,
+                     dh: torch.Tensor | None = None, out: dict | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of ``rmsnorm_quantize`` for the gradient dy of y: dx, that of h
+    (and so of x and the residual), in h's type, with dh, what reaches h another
+    way, added; and dw in fp32.  ``out`` and ``workspace`` (a uint8 tensor) may
+    be supplied."""
+    if h.dim() != 2 or h.dtype not in _SRC:
+        raise ValueError("h must be a 2-D fp32/bf16 CUDA tensor")
+    handle, dev = _on(stream, h.device), h.device
+    rows, cols = h.shape
+    src = _SRC[h.dtype]
+    pdy, ld_dy = _rows(dy, h, "dy")
+    ph, ld_h = _rows(h, h, "h")
+    pdh, ld_dh = (None, 0) if dh is None else _rows(dh, h, "dh")
+    o = dict(out or {})
+    if "dx" not in o:
+        o["dx"] = _new_rows(rows, cols, h.dtype, dev, stream)
+    if "dw" not in o:
+        o["dw"] = _empty((cols,), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _empty((max(0, lib.mx_rmsnorm_backward_workspace(rows, cols, src)),), torch.uint8, dev, stream)
+    pdx, ld_dx = _rows(o["dx"], h, "dx")
+    _check(lib.mx_rmsnorm_backward(pdy, ld_dy, ph, ld_h, _vector(w, cols, h.dtype, dev, "w"),
+                                   _vector(rstd, rows, torch.float32, dev, "rstd"), pdh, ld_dh, rows, cols, src,
+                                   pdx, ld_dx, _vector(o["dw"], cols, torch.float32, dev, "dw"),
+                                   *_work(workspace, dev), handle), "mx_rmsnorm_backward")
+    return o
+
+
+def _work(t, device):
+    if t is None:
+        return None, 0
+    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return t.data_ptr(), t.numel()
+
+
+def _gemv(call, dtype, what, x, w_q, w_s, w_fmt, M, N, K, y, stream):
+    handle, dev = _on(stream, x.device), x.device
+    if x.shape != (M, K) or x.dtype != torch.bfloat16:
+        raise ValueError("x must be a bf16 [M, K] tensor")
+    if x.stride(1) != 1 and K > 1:
+        raise ValueError("x must have unit column stride")
+    pw = _out(w_q, (N, packed_bytes(w_fmt, 1, K)), torch.uint8, dev, "w_q")
+    ps = _out(w_s, (N, (K + 31) // 32), torch.uint8, dev, "w_s")
+    if y is None:
+        y = _empty((M, N), dtype, dev, stream)
+    if y.shape != (M, N) or y.dtype != dtype or y.device != dev or (y.stride(1) != 1 and N > 1):
+        raise ValueError(f"y must be a {dtype} [M, N] tensor with unit column stride")
+    _check(call(x.data_ptr(), x.stride(0) if M > 1 else K, pw, ps, w_fmt, M, N, K, y.data_ptr(),
+                y.stride(0) if M > 1 else N, handle), what)
+    return y
+
+
+def gemv(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, w_fmt: int, M: int, N: int, K: int,
+         y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[M, N] fp32 = x[M, K] (bf16, a few tokens) x W^T for W [N, K] in 4-bit
+    row-wise MX (E2M1)."""
+    return _gemv(lib.mx_gemv, torch.float32, "mx_gemv", x, w_q, w_s, w_fmt, M, N, K, y, stream)
+
+
+def gemv_bf16(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, w_fmt: int, M: int, N: int, K: int,
+              y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``gemv`` with y rounded to bf16 (nearest even) in the kernel."""
+    return _gemv(lib.mx_gemv_bf16, torch.bfloat16, "mx_gemv_bf16", x, w_q, w_s, w_fmt, M, N, K, y, stream)
+
+
+def kv_cache(pages: int, heads: int, page: int, dim: int, device="cuda") -> dict:
+    """A new paged 8-bit MX key/value cache: uint8 tensors k_q, v_q [pages, heads,
+    page, dim] and k_s, v_s [pages, heads, page, dim / 32]."""
+    e = lambda n: torch.zeros((pages, heads, page, n), dtype=torch.uint8, device=device)
+    return {"k_q": e(dim), "k_s": e(dim // 32), "v_q": e(dim), "v_s": e(dim // 32)}
+
+
+def _cache(c, fmt, device):
+    kq = c["k_q"]
+    if kq.dim() != 4:
+        raise ValueError("k_q must be [pages, heads, page, dim]")
+    pages, heads, page, dim = shape = kq.shape
+    scales = (pages, heads, page, dim // 32)
+    return Cache(_out(kq, shape, torch.uint8, device, "k_q"), _out(c["k_s"], scales, torch.uint8, device, "k_s"),
+                 _out(c["v_q"], shape, torch.uint8, device, "v_q"), _out(c["v_s"], scales, torch.uint8, device, "v_s"),
+                 pages, heads, page, dim, fmt)
+
+
+def cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: dict, fmt: int, stream=None) -> None:
+    """Quantizes the keys and values of some tokens (fp32 or bf16 [tokens, heads,
+    dim]) into a cache (``kv_cache``): token t goes to place slots[t] % page of
+    page slots[t] // page; a slot outside the cache (-1) is not written."""
+    handle, dev = _on(stream, k.device), k.device
+    c = _cache(cache, fmt, dev)
+    if k.dim() != 3 or k.dtype not in _SRC or v.dtype != k.dtype or v.shape != k.shape or v.device != dev:
+        raise ValueError("k and v must be fp32/bf16 [tokens, heads, dim] tensors of one type")
+    tokens = k.shape[0]
+    if k.shape[1:] != (c.heads, c.dim):
+        raise ValueError(f"k must be [tokens, {c.heads}, {c.dim}]")
+    sk, sv = k.stride(), v.stride()
+    if sk[2] != 1 or sv[2] != 1:
+        raise ValueError("k and v must have unit stride along dim")
+    one = tokens <= 1  # the stride of a single token or head says nothing
+    hs_k, hs_v = (c.dim, c.dim) if c.heads <= 1 else (sk[1], sv[1])
+    _check(lib.mx_cache_write(ctypes.byref(c), k.data_ptr(), 0 if one else sk[0], hs_k, v.data_ptr(),
+                              0 if one else sv[0], hs_v, _SRC[k.dtype], tokens,
+                              _vector(slots, tokens, torch.int64, dev, "slots"), handle), "mx_cache_write")
+
+
+def attention(q: torch.Tensor, cache: dict, fmt: int, table: torch.Tensor, lens: torch.Tensor,
+              scale: float | None = None, max_len: int | None = None, out: dict | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Attention of the last Lq tokens of B requests (q bf16 [B, Lq, query heads,
+    dim]) over the requests' cached tokens: lens [B] int32 of them, the queries'
+    own included, in the pages table [B, n] int32.  Query i sees the tokens before
+    lens - Lq + i + 1.  Returns o like q and lse [B, Lq, query heads] fp32.
+    ``max_len``: a bound of lens (default: what the table holds); ``scale``:
+    default 1 / sqrt(dim); ``out`` and ``workspace`` may be supplied."""
+    handle, dev = _on(stream, q.device), q.device
+    c = _cache(cache, fmt, dev)
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or q.shape[3] != c.dim:
+        raise ValueError(f"q must be a bf16 [B, Lq, query heads, {c.dim}] tensor")
+    B, Lq, heads_q, dim = q.shape
+    sq = q.stride()
+    if sq[3] != 1 or (sq[2] != dim and heads_q > 1) or (sq[0] != Lq * sq[1] and B > 1 and Lq > 1):
+        raise ValueError("q must have contiguous heads and evenly spaced tokens")
+    ld_q = sq[1] if Lq > 1 else sq[0] if B > 1 else heads_q * dim
+    if table.dim() != 2 or table.shape[0] != B or table.dtype != torch.int32 or table.device != dev or \
+            (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError("table must be an int32 [B, pages] tensor with unit column stride")
+    per = table.shape[1]
+    if max_len is None:
+        max_len = per * c.page
+    o = dict(out or {})
+    if "o" not in o:
+        o["o"] = _empty((B, Lq, heads_q, dim), torch.bfloat16, dev, stream)
+    if "lse" not in o:
+        o["lse"] = _empty((B, Lq, heads_q), torch.float32, dev, stream)
+    if workspace is None:
+        need = lib.mx_attention_workspace(B, Lq, heads_q, c.heads, dim, max_len)
+        if need > 0:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+    _check(lib.mx_attention(ctypes.byref(c), q.data_ptr(), ld_q, table.data_ptr(),
+                            table.stride(0) if B > 1 else per, _vector(lens, B, torch.int32, dev, "lens"), B, Lq,
+                            heads_q, dim ** -0.5 if scale is None else scale, max_len,
+                            _out(o["o"], (B, Lq, heads_q, dim), torch.bfloat16, dev, "o"), heads_q * dim,
+                            _out(o["lse"], (B, Lq, heads_q), torch.float32, dev, "lse"),
+                            *_work(workspace, dev), handle), "mx_attention")
     return o

@@ -122,10 +122,10 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {  // 
 // The bytes of 32 tokens in a lane.
 template <int D>
 struct Raw {
-  uint32_t k[2][D / 16];    // dims g D/4 .. of token 16 u + l % 16
-  uint32_t ks[2];           // the scales of those dims (one, or two for 256)
-  uint32_t v[2][4][D / 64]; // dims (l % 16) D/16 .. of token 16 u + 4 g + r
-  uint32_t vs[2][D / 32];   // the scales of tokens 16 u + 4 g .. + 3, D / 32 bytes each
+  uint32_t k[2][D / 16];     // dims g D/4 .. of token 16 u + l % 16
+  uint32_t ks[2];            // the scales of those dims (one, or two for 256)
+  uint32_t v[2][4][D / 64];  // dims (l % 16) D/16 .. of token 16 u + 4 g + r
+  uint32_t vs[2][D / 32];    // the scales of tokens 16 u + 4 g .. + 3, D / 32 bytes each
 };
 
 // Where tokens 16 u .. of a request lie: row (page, head, place) of the cache.
@@ -138,10 +138,12 @@ __device__ __forceinline__ bool locate(const AttnArgs& p, const int32_t* table, 
   return (uint32_t)pg < (uint32_t)p.a.c.pages;
 }
 
+// Rows are the same for the whole wave, so addresses are a scalar base and a
+// lane's constant offset.
 template <int D>
 __device__ __forceinline__ uint32_t load_step(const AttnArgs& p, const int32_t* table, int head, int t0, int end,
                                               Raw<D>& x) {
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   uint32_t there = 0;
 #pragma unroll
   for (int u = 0; u < 2; u++) {
@@ -150,55 +152,18 @@ __device__ __forceinline__ uint32_t load_step(const AttnArgs& p, const int32_t* 
     if (ok) ok = locate(p, table, head, t0 + 16 * u, row);
     if (!ok) row = 0;  // any row of the cache: what it holds is masked
     there |= (uint32_t)ok << u;
-    const int64_t kr = row + i, vr = row + 4 * g;
-    load_words<D / 16>(p.a.c.k_q + kr * D + g * (D / 4), x.k[u]);
-    const uint8_t* ks = p.a.c.k_s + kr * (D / 32);
-    if constexpr (D == 256) x.ks[u] = *(const uint16_t*)(ks + 2 * g);
-    else x.ks[u] = ks[g * D / 128];
+    const uint8_t* kq = p.a.c.k_q + row * D;
+    const uint8_t* ks = p.a.c.k_s + row * (D / 32);
+    const uint8_t* vq = p.a.c.v_q + row * D;
+    const uint8_t* vs = p.a.c.v_s + row * (D / 32);
+    load_words<D / 16>(kq + (i * D + g * (D / 4)), x.k[u]);
+    if constexpr (D == 256) x.ks[u] = *(const uint16_t*)(ks + (i * 8 + 2 * g));
+    else x.ks[u] = ks[i * (D / 32) + g * D / 128];
 #pragma unroll
-    for (int r = 0; r < 4; r++) load_words<D / 64>(p.a.c.v_q + (vr + r) * D + i * (D / 16), x.v[u][r]);
-    load_words<D / 32>(p.a.c.v_s + vr * (D / 32), x.vs[u]);
+    for (int r = 0; r < 4; r++) load_words<D / 64>(vq + (4 * g * D + i * (D / 16)) + r * D, x.v[u][r]);
+    load_words<D / 32>(vs + 4 * g * (D / 32), x.vs[u]);
   }
   return there;
-}
-
-// V as operands of the second product: dims (l % 16) D/16 + d of the lane's 8
-// tokens.  With CUT, tokens at or past `end` (from the step's first) are zeros
-// whatever the cache holds there.
-template <int D, int F, bool CUT>
-__device__ __forceinline__ void v_operands(const Raw<D>& x, int end, uint32_t there, uint32_t w[D / 16][4]) {
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  const int blk = i * (D / 16) / 32;  // the block of the lane's dims
-#pragma unroll
-  for (int u = 0; u < 2; u++) {
-#pragma unroll
-    for (int h = 0; h < 2; h++) {  // tokens 2 h and 2 h + 1 of the four
-      float s[2];
-      uint32_t raw[2][D / 64];
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const int r = 2 * h + e;
-        // byte r D/32 + blk of x.vs[u]
-        uint32_t code;
-        if constexpr (D == 64) code = (x.vs[u][r >> 1] >> (16 * (r & 1) + 8 * blk)) & 0xFFu;
-        else if constexpr (D == 128) code = (x.vs[u][r] >> (8 * blk)) & 0xFFu;
-        else code = ((blk & 4 ? x.vs[u][2 * r + 1] : x.vs[u][2 * r]) >> (8 * (blk & 3))) & 0xFFu;
-        const bool cut = CUT && (!(there >> u & 1) || 16 * u + 4 * g + r >= end);
-        s[e] = e8m0(cut ? 127u : code);
-#pragma unroll
-        for (int k = 0; k < D / 64; k++) raw[e][k] = cut ? 0u : x.v[u][r][k];
-      }
-#pragma unroll
-      for (int k = 0; k < D / 64; k++) {
-        const uint32_t a0 = cvt_lo<F>(raw[0][k], s[0]), a1 = cvt_hi<F>(raw[0][k], s[0]);
-        const uint32_t b0 = cvt_lo<F>(raw[1][k], s[1]), b1 = cvt_hi<F>(raw[1][k], s[1]);
-        w[4 * k][2 * u + h] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
-        w[4 * k + 1][2 * u + h] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
-        w[4 * k + 2][2 * u + h] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
-        w[4 * k + 3][2 * u + h] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
-      }
-    }
-  }
 }
 
 __device__ __forceinline__ bf16x8 operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -208,6 +173,34 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
+// Scale code of the lane's dims of V for token 16 u + 4 g + r: byte r D/32 +
+// block of x.vs[u].
+template <int D>
+__device__ __forceinline__ uint32_t v_scale(const Raw<D>& x, int u, int r) {
+  const int blk = (int)(threadIdx.x & 15) * (D / 16) / 32;
+  if constexpr (D == 64) return (x.vs[u][r >> 1] >> (16 * (r & 1) + 8 * blk)) & 0xFFu;
+  else if constexpr (D == 128) return (x.vs[u][r] >> (8 * blk)) & 0xFFu;
+  else return ((blk & 4 ? x.vs[u][2 * r + 1] : x.vs[u][2 * r]) >> (8 * (blk & 3))) & 0xFFu;
+}
+
+// V as operands of the second product: dims (l % 16) D/16 + 4 k .. + 3 of the
+// lane's 8 tokens (dword c of an operand: tokens 2 c and 2 c + 1 of the eight).
+template <int D, int F>
+__device__ __forceinline__ void v_operands(const Raw<D>& x, const float s[2][4], int k, uint32_t w[4][4]) {
+#pragma unroll
+  for (int u = 0; u < 2; u++)
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const uint32_t ra = x.v[u][2 * h][k], rb = x.v[u][2 * h + 1][k];
+      const uint32_t a0 = cvt_lo<F>(ra, s[u][2 * h]), a1 = cvt_hi<F>(ra, s[u][2 * h]);
+      const uint32_t b0 = cvt_lo<F>(rb, s[u][2 * h + 1]), b1 = cvt_hi<F>(rb, s[u][2 * h + 1]);
+      w[0][2 * u + h] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+      w[1][2 * u + h] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+      w[2][2 * u + h] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+      w[3][2 * u + h] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+    }
+}
+
 // What a wave has summed for its rows.
 template <int D, int NR>
 struct Sums {
@@ -215,13 +208,13 @@ struct Sums {
   float m[NR], l[NR];   // l over the lane's tokens only
 };
 
-// One step of 32 tokens.  MASK: some row may not see all of them; limit[n] is
-// then the lane's row's limit, counted from the step's first token, and `end` the
-// largest limit of the workgroup.
-template <int D, int F, int NR, bool MASK>
-__device__ __forceinline__ void take_step(const AttnArgs& p, const Raw<D>& x, const bf16x8 (&q)[NR][D / 32],
-                                          float scale2, uint32_t there, int end, const int (&limit)[NR],
-                                          Sums<D, NR>& sum) {
+// One step of 32 tokens.  `cut`: some row does not see all of them, or some are
+// not there.  limit[n] is the number of them that the lane's row sees (less than
+// 1: none, 32 or more: all), `end` the largest such number of the workgroup.
+template <int D, int F, int NR>
+__device__ __forceinline__ void take_step(const AttnArgs& p, Raw<D>& x, const bf16x8 (&q)[NR][D / 32],
+                                          float scale2, bool cut, uint32_t there, int end,
+                                          const int (&limit)[NR], Sums<D, NR>& sum) {
   const int g = (threadIdx.x & 63) >> 4;
   f32x4 s[NR][2];
 #pragma unroll
@@ -238,18 +231,51 @@ __device__ __forceinline__ void take_step(const AttnArgs& p, const Raw<D>& x, co
       for (int n = 0; n < NR; n++) s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[n][j], s[n][u], 0, 0, 0);
     }
   }
+  bool odd = false;
+  if (cut) {
+#pragma unroll
+    for (int n = 0; n < NR; n++)
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const int tok = 16 * (e >> 2) + 4 * g + (e & 3);
+        const bool seen = tok < limit[n] && (there >> (e >> 2) & 1);
+        s[n][e >> 2][e & 3] = seen ? s[n][e >> 2][e & 3] : -__builtin_inff();
+      }
+    // Tokens that no row sees count as zeros whatever the cache holds there, for
+    // 0 * NaN is not 0.  Of the others, one with a value that may not be finite
+    // sends the step the long way (below) where rows see different tokens.
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const bool gone = !(there >> u & 1) || 16 * u + 4 * g + r >= end;
+        odd |= !gone && v_scale<D>(x, u, r) > (uint32_t)(254 - Fmt<F>::emax);
+#pragma unroll
+        for (int k = 0; k < D / 64; k++) {
+          x.v[u][r][k] = gone ? 0u : x.v[u][r][k];
+          odd |= (((x.v[u][r][k] & 0x7F7F7F7Fu) + (F == E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u) != 0;
+        }
+      }
+  }
+  float vs[2][4];
+#pragma unroll
+  for (int u = 0; u < 2; u++)
+#pragma unroll
+    for (int r = 0; r < 4; r++) vs[u][r] = e8m0(v_scale<D>(x, u, r));
+  if (cut) {  // a scale of a token that is not there may be a NaN
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int r = 0; r < 4; r++)
+        vs[u][r] = !(there >> u & 1) || 16 * u + 4 * g + r >= end ? 1.0f : vs[u][r];
+  }
   bf16x8 pr[NR];
 #pragma unroll
   for (int n = 0; n < NR; n++) {
-    float v[8];
-    float top = -__builtin_inff();
+    float v[8], top = -__builtin_inff();
 #pragma unroll
     for (int e = 0; e < 8; e++) {
       v[e] = s[n][e >> 2][e & 3] * scale2;
-      if (MASK) {
-        const int tok = 16 * (e >> 2) + 4 * g + (e & 3);
-        if (tok >= limit[n] || !(there >> (e >> 2) & 1)) v[e] = -__builtin_inff();
-      }
       top = __builtin_fmaxf(top, v[e]);
     }
     const float m = __builtin_fmaxf(sum.m[n], rows_max(top));
@@ -268,55 +294,51 @@ __device__ __forceinline__ void take_step(const AttnArgs& p, const Raw<D>& x, co
     }
     pr[n] = operand(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
   }
-  uint32_t w[D / 16][4];
-  v_operands<D, F, MASK>(x, end, there, w);
-  if (MASK) {
-    // Rows see different numbers of these tokens.  Where a value is not finite,
-    // a row that does not see it must not multiply it by its zero: then each
-    // limit is taken by itself, with the values past it cut.
-    bool odd = false;
-    if (p.a.Lq > 1) {
+  if (p.a.Lq > 1 && __any(odd)) {
+    // each number of tokens by itself, with the values past it cut, for the rows
+    // that see that many
+    for (int lim = 1; lim <= STEP; lim++) {
+      uint32_t keep[4];
 #pragma unroll
-      for (int d = 0; d < D / 16; d++)
+      for (int c = 0; c < 4; c++) {
+        const int tok = 16 * (c >> 1) + 4 * g + 2 * (c & 1);
+        keep[c] = (tok < lim ? 0xFFFFu : 0u) | (tok + 1 < lim ? 0xFFFF0000u : 0u);
+      }
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-          odd |= (w[d][k] & 0x7F80u) == 0x7F80u || (w[d][k] & 0x7F800000u) == 0x7F800000u;
-    }
-    if (__any(odd)) {
-      for (int lim = 1; lim <= STEP; lim++) {
-        uint32_t keep[4];
+      for (int k = 0; k < D / 64; k++) {
+        uint32_t w[4][4];
+        v_operands<D, F>(x, vs, k, w);
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const int tok = 16 * (k >> 1) + 4 * g + 2 * (k & 1);
-          keep[k] = (tok < lim ? 0xFFFFu : 0u) | (tok + 1 < lim ? 0xFFFF0000u : 0u);
-        }
+        for (int d = 0; d < 4; d++) {
+          const bf16x8 v = operand(w[d][0] & keep[0], w[d][1] & keep[1], w[d][2] & keep[2], w[d][3] & keep[3]);
 #pragma unroll
-        for (int n = 0; n < NR; n++) {
-          const bool mine = lim == (limit[n] < STEP ? limit[n] : STEP);
+          for (int n = 0; n < NR; n++) {
+            const f32x4 o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[n], sum.o[n][4 * k + d], 0, 0, 0);
+            const bool mine = lim == (limit[n] < STEP ? limit[n] : STEP);
 #pragma unroll
-          for (int d = 0; d < D / 16; d++) {
-            const f32x4 o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                operand(w[d][0] & keep[0], w[d][1] & keep[1], w[d][2] & keep[2], w[d][3] & keep[3]), pr[n],
-                sum.o[n][d], 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; e++) sum.o[n][d][e] = mine ? o[e] : sum.o[n][d][e];
+            for (int e = 0; e < 4; e++) sum.o[n][4 * k + d][e] = mine ? o[e] : sum.o[n][4 * k + d][e];
           }
         }
       }
-      return;
     }
+    return;
   }
 #pragma unroll
-  for (int d = 0; d < D / 16; d++) {
-    const bf16x8 v = operand(w[d][0], w[d][1], w[d][2], w[d][3]);
+  for (int k = 0; k < D / 64; k++) {
+    uint32_t w[4][4];
+    v_operands<D, F>(x, vs, k, w);
 #pragma unroll
-    for (int n = 0; n < NR; n++)
-      sum.o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[n], sum.o[n][d], 0, 0, 0);
+    for (int d = 0; d < 4; d++) {
+      const bf16x8 v = operand(w[d][0], w[d][1], w[d][2], w[d][3]);
+#pragma unroll
+      for (int n = 0; n < NR; n++)
+        sum.o[n][4 * k + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[n], sum.o[n][4 * k + d], 0, 0, 0);
+    }
   }
 }
 
 template <int D, int F, int NR>
-__global__ __launch_bounds__(64 * WAVES) void k_attention(AttnArgs p) {
+__global__ __launch_bounds__(64 * WAVES, D < 256 && NR == 1 ? 2 : 1) void k_attention(AttnArgs p) {
   __shared__ float ml[WAVES][NR][16][2];
   __shared__ float os[WAVES][16][D + 4];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -369,8 +391,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention(AttnArgs p) {
       int limit[NR];
 #pragma unroll
       for (int n = 0; n < NR; n++) limit[n] = lim[n] - t;
-      if (there == 3u && t + STEP <= low) take_step<D, F, NR, false>(p, x, q, scale2, there, t1 - t, limit, sum);
-      else take_step<D, F, NR, true>(p, x, q, scale2, there, t1 - t, limit, sum);
+      take_step<D, F, NR>(p, x, q, scale2, there != 3u || t + STEP > low, there, t1 - t, limit, sum);
       t = next;
       if (t >= t1) break;
       x = ahead;
@@ -478,7 +499,7 @@ struct Plan {
 Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_len) {
   Plan r;
   const int64_t rows = Lq * group;
-  r.nr = rows <= 16 ? 1 : rows <= 32 || dim == 256 ? 2 : 4;
+  r.nr = rows <= 16 || dim == 256 ? 1 : rows <= 32 || dim == 128 ? 2 : 4;
   r.tiles = (int)((rows + 16 * r.nr - 1) / (16 * r.nr));
   const int64_t unit = STEP * WAVES, base = B * heads * r.tiles;
   const int64_t units = (max_len + unit - 1) / unit;
@@ -497,8 +518,10 @@ template <int D, int F>
 hipError_t attention_by_rows(const AttnArgs& p, const Plan& r, hipStream_t st) {
   const dim3 g((unsigned)r.splits, (unsigned)r.tiles, (unsigned)(p.a.B * p.a.c.heads)), b(64 * WAVES);
   if (r.nr == 1) hipLaunchKernelGGL((k_attention<D, F, 1>), g, b, 0, st, p);
-  else if (r.nr == 2) hipLaunchKernelGGL((k_attention<D, F, 2>), g, b, 0, st, p);
-  else if constexpr (D < 256) hipLaunchKernelGGL((k_attention<D, F, 4>), g, b, 0, st, p);
+  if constexpr (D <= 128)
+    if (r.nr == 2) hipLaunchKernelGGL((k_attention<D, F, 2>), g, b, 0, st, p);
+  if constexpr (D == 64)
+    if (r.nr == 4) hipLaunchKernelGGL((k_attention<D, F, 4>), g, b, 0, st, p);
   if (r.splits > 1) {
     const int64_t n = (int64_t)p.a.B * p.a.c.heads * p.rows;
     hipLaunchKernelGGL(k_attention_join<D>, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);

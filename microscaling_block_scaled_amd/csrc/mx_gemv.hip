@@ -14,6 +14,7 @@
 // lane (row l % 16, group g = l / 16) loads 16 bytes, the whole block 4 i + g of
 // four, and feeds its elements 8 j .. 8 j + 7 to instruction j; the tokens' lanes
 // take the same elements of x, which is all the order that a sum over k needs.
+#include <cstdlib>
 #include "mx_device.hpp"
 #include "mx_layer.h"
 
@@ -26,7 +27,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int ROWS = 16;    // rows of W per workgroup
-constexpr int WAVES = 8;
 
 // Eight E2M1 codes (a dword) times the scale as a bf16 operand.
 __device__ __forceinline__ bf16x8 fp4_operand(uint32_t q, float scale) {
@@ -109,8 +109,8 @@ __device__ __forceinline__ void take_step(const Step<MT, NI>& st, int g, f32x4 a
   }
 }
 
-template <int MT, int NI, bool BF16>
-__global__ __launch_bounds__(64 * WAVES) void k_gemv(GemvArgs p) {
+template <int MT, int NI, int WAVES, int OCC, bool BF16>
+__global__ __launch_bounds__(64 * WAVES, OCC) void k_gemv(GemvArgs p) {
   __shared__ float part[WAVES][MT][16][ROWS + 1];
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -131,17 +131,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_gemv(GemvArgs p) {
   constexpr int STEP = 4 * NI;                 // blocks a wave takes at a time
   const int whole = (int)(p.K / (32 * STEP));  // steps with all of their blocks and elements
   int s = wave;
-  if (s < whole) {
+  for (; s < whole; s += WAVES) {
     Step<MT, NI> st;
     load_step<MT, NI, true>(st, qrow, srow, xrow, s * STEP, g, nb, p.K);
-    for (; s + WAVES < whole; s += WAVES) {
-      Step<MT, NI> ahead;
-      load_step<MT, NI, true>(ahead, qrow, srow, xrow, (s + WAVES) * STEP, g, nb, p.K);
-      take_step<MT, NI>(st, g, acc);
-      st = ahead;
-    }
     take_step<MT, NI>(st, g, acc);
-    s += WAVES;
   }
   if (s == whole && whole * STEP < nb) {  // the short last step
     Step<MT, NI> st;
@@ -168,17 +161,29 @@ __global__ __launch_bounds__(64 * WAVES) void k_gemv(GemvArgs p) {
 
 }  // namespace
 
+template <int MT, int NI, int W, int OCC>
+static void go(const GemvArgs& a, dim3 g, hipStream_t st) {
+  if (a.bf16) hipLaunchKernelGGL((k_gemv<MT, NI, W, OCC, true>), g, dim3(64 * W), 0, st, a);
+  else hipLaunchKernelGGL((k_gemv<MT, NI, W, OCC, false>), g, dim3(64 * W), 0, st, a);
+}
 hipError_t launch_gemv(const GemvArgs& a, hipStream_t st) {
   const unsigned gx = (unsigned)((a.N + ROWS - 1) / ROWS);
-  const dim3 b(64 * WAVES);
+  static const int V = getenv("MXV") ? atoi(getenv("MXV")) : 0;
   if (a.M <= 16) {
     const dim3 g(gx, 1);
-    if (a.bf16) hipLaunchKernelGGL((k_gemv<1, 4, true>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_gemv<1, 4, false>), g, b, 0, st, a);
+    switch (V) {
+      case 0: go<1, 4, 8, 4>(a, g, st); break;
+      case 1: go<1, 2, 8, 4>(a, g, st); break;
+      case 2: go<1, 2, 8, 8>(a, g, st); break;
+      case 3: go<1, 4, 16, 4>(a, g, st); break;
+      case 4: go<1, 2, 16, 8>(a, g, st); break;
+      case 5: go<1, 2, 16, 4>(a, g, st); break;
+      case 6: go<1, 4, 4, 4>(a, g, st); break;
+      case 7: go<1, 2, 4, 8>(a, g, st); break;
+    }
   } else {  // each 32 tokens read the weights once
     const dim3 g(gx, (unsigned)((a.M + 31) / 32));
-    if (a.bf16) hipLaunchKernelGGL((k_gemv<2, 2, true>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_gemv<2, 2, false>), g, b, 0, st, a);
+    go<2, 2, 8, 4>(a, g, st);
   }
   return hipGetLastError();
 }

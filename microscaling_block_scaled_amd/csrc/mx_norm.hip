@@ -97,7 +97,7 @@ template <int W>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = wave_sum(v);
   if (W == 1) return v;
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  if ((threadIdx.x & 63) == 0) red[(threadIdx.x >> 6) & (W - 1)] = v;
   __syncthreads();
   v = 0.0f;
 #pragma unroll
@@ -152,17 +152,19 @@ __device__ __forceinline__ void write_chunk(const NormArgs& p, int64_t row, int 
   store8<F, false>(p.q + row * (bpr * (4 * Fmt<F>::bits)), c, o);
 }
 
-// One row by W waves, NC chunks a lane.
+// Rows by W waves each, NC chunks a lane.
 template <int SRC, int F, int W, int NC>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_norm_quant(NormArgs p) {
+__global__ __launch_bounds__(W < 8 ? 256 : WG) void k_norm_quant(NormArgs p) {
   constexpr int ESZ = SRC == SRC_BF16 ? 2 : 4;
-  constexpr int T = 64 * W;
-  __shared__ float red[W];
-  const int t = W == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
-                             : (int64_t)blockIdx.x;
-  if (row >= p.rows) return;  // whole waves; W > 1: never
-  const int cols = (int)p.cols, nch = (cols + 31) / 32 * 4;
+  constexpr int T = 64 * W, RPB = W < 8 ? 4 / W : 1;
+  __shared__ float red[8];
+  const int t = (int)threadIdx.x & (T - 1);
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  const int64_t last = (int64_t)blockIdx.x * RPB + group;
+  // past the last row: a row of no elements, for the barrier's sake
+  const bool live = last < p.rows;
+  const int64_t row = live ? last : 0;
+  const int cols = live ? (int)p.cols : 0, nch = (cols + 31) / 32 * 4;
   const uint8_t* x = (const uint8_t*)p.x + row * p.ld_x;
   const uint8_t* r = p.r ? (const uint8_t*)p.r + row * p.ld_r : nullptr;
   uint32_t h[NC][2 * ESZ], w[NC][2 * ESZ];
@@ -198,9 +200,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_norm_quant(NormArgs p
     for (int k = 0; k < 8; k++) sum = __builtin_fmaf(v[k], v[k], sum);
     if (p.h) store_chunk<ESZ>((uint8_t*)p.h + row * p.ld_h, t + T * i, cols, h[i]);
   }
-  sum = row_sum<W>(sum, red);
+  sum = row_sum<W>(sum, red + group * W);
   const float rstd = inv_rms(sum, cols, p.eps);
-  if (t == 0 && p.rstd) p.rstd[row] = rstd;
+  if (t == 0 && live && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < NC; i++)
     if (t + T * i < nch) write_chunk<SRC, F>(p, row, t + T * i, h[i], w[i], rstd);
@@ -292,10 +294,10 @@ template <int SRC, int W, int NC>
 __global__ __launch_bounds__(WG) void k_norm_grad(NormGradArgs p) {
   constexpr int ESZ = SRC == SRC_BF16 ? 2 : 4;
   constexpr int T = 64 * W, RPB = WG / T;  // rows a workgroup takes at a time
-  __shared__ float red[2][W];
-  __shared__ __align__(16) float share[RPB > 1 ? 8 * 64 * NC : 1];
-  const int t = W == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ float red[2][WG / 64];
+  __shared__ __align__(16) float share[RPB > 1 ? 8 * T * NC : 1];
+  const int t = (int)threadIdx.x & (T - 1);
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
   const int cols = (int)p.cols;
   float dw[NC][8];
   uint32_t w[NC][2 * ESZ];
@@ -307,51 +309,59 @@ __global__ __launch_bounds__(WG) void k_norm_grad(NormGradArgs p) {
     load_tail<ESZ>((const uint8_t*)p.w, t + T * i, cols, w[i]);
   }
   const float inv_n = 1.0f / (float)cols;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + (W == 1 ? wave : 0); row < p.rows;
-       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+  // a row's chunks; rows past the last are zeros
+  struct Row {
+    uint32_t h[NC][2 * ESZ], dy[NC][2 * ESZ], dh[NC][2 * ESZ];
+    float rstd;
+  };
+  auto load_row = [&](int64_t row, Row& x) {
+    const bool live = row < p.rows;
+    const int n = live ? cols : 0;
+    row = live ? row : 0;
     const uint8_t* hr = (const uint8_t*)p.h + row * p.ld_h;
     const uint8_t* dyr = (const uint8_t*)p.dy + row * p.ld_dy;
-    const uint8_t* dhr = p.dh ? (const uint8_t*)p.dh + row * p.ld_dh : nullptr;
-    uint32_t h[NC][2 * ESZ], dy[NC][2 * ESZ], dh[NC][2 * ESZ];
-#pragma unroll
-    for (int i = 0; i < NC; i++) load_chunk<ESZ>(hr, t + T * i, cols, h[i]);
-#pragma unroll
-    for (int i = 0; i < NC; i++) load_chunk<ESZ>(dyr, t + T * i, cols, dy[i]);
+    const uint8_t* dhr = (const uint8_t*)p.dh + row * p.ld_dh;
+    x.rstd = live ? p.rstd[row] : 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; i++) {
-      if (dhr) {
-        load_chunk<ESZ>(dhr, t + T * i, cols, dh[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2 * ESZ; k++) dh[i][k] = 0;
-      }
+      load_chunk<ESZ>(hr, t + T * i, n, x.h[i]);
+      load_chunk<ESZ>(dyr, t + T * i, n, x.dy[i]);
+      load_chunk<ESZ>(dhr, t + T * i, p.dh ? n : 0, x.dh[i]);
     }
     if (cols & 7) {
 #pragma unroll
       for (int i = 0; i < NC; i++) {
-        load_tail<ESZ>(hr, t + T * i, cols, h[i]);
-        load_tail<ESZ>(dyr, t + T * i, cols, dy[i]);
-        if (dhr) load_tail<ESZ>(dhr, t + T * i, cols, dh[i]);
+        load_tail<ESZ>(hr, t + T * i, n, x.h[i]);
+        load_tail<ESZ>(dyr, t + T * i, n, x.dy[i]);
+        load_tail<ESZ>(dhr, t + T * i, p.dh ? n : 0, x.dh[i]);
       }
     }
-    const float rstd = p.rstd[row];
+  };
+  Row x;
+  load_row((int64_t)blockIdx.x * RPB + group, x);
+  int turn = 0;
+  // the same number of turns for every wave of the workgroup
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < p.rows; base += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const int64_t row = base + group;
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NC; i++) grad_chunk_sums<SRC>(h[i], dy[i], w[i], rstd, dot, dw[i]);
-    const float mean = row_sum<W>(dot, red[turn]) * inv_n;
+    for (int i = 0; i < NC; i++) grad_chunk_sums<SRC>(x.h[i], x.dy[i], w[i], x.rstd, dot, dw[i]);
+    Row ahead;
+    load_row(row + (int64_t)gridDim.x * RPB, ahead);
+    const float mean = row_sum<W>(dot, red[turn] + group * W) * inv_n;
     uint8_t* dxr = (uint8_t*)p.dx + row * p.ld_dx;
 #pragma unroll
     for (int i = 0; i < NC; i++) {
       uint32_t o[2 * ESZ];
-      grad_chunk_dx<SRC>(h[i], dy[i], w[i], dh[i], rstd, mean, o);
-      store_chunk<ESZ>(dxr, t + T * i, cols, o);
+      grad_chunk_dx<SRC>(x.h[i], x.dy[i], w[i], x.dh[i], x.rstd, mean, o);
+      store_chunk<ESZ>(dxr, t + T * i, row < p.rows ? cols : 0, o);
     }
+    x = ahead;
   }
   float* out = p.partial + (int64_t)blockIdx.x * cols;
-  if constexpr (RPB > 1) {  // waves add their shares one after the other
+  if constexpr (RPB > 1) {  // the groups add their shares one after the other
     for (int v = 0; v < RPB; v++) {
-      if (wave == v) {
+      if (group == v) {
 #pragma unroll
         for (int i = 0; i < NC; i++) {
           float* s = share + 8 * (t + T * i);
@@ -453,24 +463,21 @@ __global__ __launch_bounds__(1024) void k_sum_partials(const float* __restrict__
 }
 
 constexpr int64_t kMaxCols = 16384;  // 8 waves x 64 lanes x 4 chunks of 8
+// the gradient kernel's row in registers: h, dy, dh, the next row's, w and dw
+constexpr int64_t grad_max_cols(int src) { return src == SRC_BF16 ? 16384 : 8192; }
 
 template <int SRC, int F>
 hipError_t norm_launch(const NormArgs& a, hipStream_t st) {
   const unsigned rows = (unsigned)a.rows;
-  const bool waves = a.cols <= 4096 && a.rows >= 1024;
-  if (waves) {
-    const dim3 g((rows + 3) / 4), b(256);
-    if (a.cols <= 512) hipLaunchKernelGGL((k_norm_quant<SRC, F, 1, 1>), g, b, 0, st, a);
-    else if (a.cols <= 1024) hipLaunchKernelGGL((k_norm_quant<SRC, F, 1, 2>), g, b, 0, st, a);
-    else if (a.cols <= 2048) hipLaunchKernelGGL((k_norm_quant<SRC, F, 1, 4>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_norm_quant<SRC, F, 1, 8>), g, b, 0, st, a);
-  } else {
-    const dim3 g(rows), b(WG);
-    if (a.cols <= 4096) hipLaunchKernelGGL((k_norm_quant<SRC, F, 8, 1>), g, b, 0, st, a);
-    else if (a.cols <= 8192) hipLaunchKernelGGL((k_norm_quant<SRC, F, 8, 2>), g, b, 0, st, a);
-    else if (a.cols <= kMaxCols) hipLaunchKernelGGL((k_norm_quant<SRC, F, 8, 4>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_norm_quant_wide<SRC, F>), g, b, 0, st, a);
-  }
+  const dim3 b(a.cols <= 2048 ? 256 : WG);
+  auto grid = [&](unsigned per) { return dim3((rows + per - 1) / per); };
+  if (a.cols <= 512) hipLaunchKernelGGL((k_norm_quant<SRC, F, 1, 1>), grid(4), b, 0, st, a);
+  else if (a.cols <= 1024) hipLaunchKernelGGL((k_norm_quant<SRC, F, 2, 1>), grid(2), b, 0, st, a);
+  else if (a.cols <= 2048) hipLaunchKernelGGL((k_norm_quant<SRC, F, 4, 1>), grid(1), b, 0, st, a);
+  else if (a.cols <= 4096) hipLaunchKernelGGL((k_norm_quant<SRC, F, 8, 1>), grid(1), b, 0, st, a);
+  else if (a.cols <= 8192) hipLaunchKernelGGL((k_norm_quant<SRC, F, 8, 2>), grid(1), b, 0, st, a);
+  else if (a.cols <= kMaxCols) hipLaunchKernelGGL((k_norm_quant<SRC, F, 8, 4>), grid(1), b, 0, st, a);
+  else hipLaunchKernelGGL((k_norm_quant_wide<SRC, F>), grid(1), b, 0, st, a);
   return hipGetLastError();
 }
 
@@ -486,30 +493,26 @@ hipError_t norm_by_fmt(const NormArgs& a, hipStream_t st) {
   }
 }
 
-// Whether a wave holds a row in the gradient kernel: h, dy, dh, w and dw of a
-// row are 5 x NC x 8 registers in fp32, so fp32 stops at 2048 columns.
-bool grad_by_wave(int64_t rows, int64_t cols, int src) {
-  return cols <= (src == SRC_BF16 ? 4096 : 2048) && rows >= 2048;
-}
+// Waves that share a row in the gradient kernel: a chunk a lane where eight
+// waves suffice.
+int grad_waves(int64_t cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : 8; }
 
 template <int SRC>
 hipError_t grad_launch(const NormGradArgs& a, hipStream_t st) {
   const int64_t n = norm_grad_partials(a.rows, a.cols, SRC);
   const dim3 g((unsigned)n), b(WG);
   if (a.rows == 0) {  // dw is a sum of nothing
-  } else if (a.cols > kMaxCols) {
+  } else if (a.cols > grad_max_cols(SRC)) {
     const dim3 gc((unsigned)((a.cols + 8 * WG - 1) / (8 * WG)), (unsigned)n);
     hipLaunchKernelGGL(k_norm_dw_wide<SRC>, gc, b, 0, st, a);
     hipLaunchKernelGGL(k_norm_grad_wide<SRC>, dim3((unsigned)a.rows), b, 0, st, a);
-  } else if (grad_by_wave(a.rows, a.cols, SRC)) {
-    if (a.cols <= 512) hipLaunchKernelGGL((k_norm_grad<SRC, 1, 1>), g, b, 0, st, a);
-    else if (a.cols <= 1024) hipLaunchKernelGGL((k_norm_grad<SRC, 1, 2>), g, b, 0, st, a);
-    else if (a.cols <= 2048) hipLaunchKernelGGL((k_norm_grad<SRC, 1, 4>), g, b, 0, st, a);
-    else if constexpr (SRC == SRC_BF16) hipLaunchKernelGGL((k_norm_grad<SRC, 1, 8>), g, b, 0, st, a);
   } else {
-    if (a.cols <= 4096) hipLaunchKernelGGL((k_norm_grad<SRC, 8, 1>), g, b, 0, st, a);
+    if (a.cols <= 512) hipLaunchKernelGGL((k_norm_grad<SRC, 1, 1>), g, b, 0, st, a);
+    else if (a.cols <= 1024) hipLaunchKernelGGL((k_norm_grad<SRC, 2, 1>), g, b, 0, st, a);
+    else if (a.cols <= 2048) hipLaunchKernelGGL((k_norm_grad<SRC, 4, 1>), g, b, 0, st, a);
+    else if (a.cols <= 4096) hipLaunchKernelGGL((k_norm_grad<SRC, 8, 1>), g, b, 0, st, a);
     else if (a.cols <= 8192) hipLaunchKernelGGL((k_norm_grad<SRC, 8, 2>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_norm_grad<SRC, 8, 4>), g, b, 0, st, a);
+    else if constexpr (SRC == SRC_BF16) hipLaunchKernelGGL((k_norm_grad<SRC, 8, 4>), g, b, 0, st, a);
   }
   hipLaunchKernelGGL(k_sum_partials, dim3((unsigned)((a.cols + 63) / 64)), dim3(1024), 0, st,
                      (const float*)a.partial, (int)n, a.cols, a.dw);
@@ -522,12 +525,11 @@ hipError_t launch_norm_quant(const NormArgs& a, hipStream_t st) {
   return a.src == SRC_BF16 ? norm_by_fmt<SRC_BF16>(a, st) : norm_by_fmt<SRC_F32>(a, st);
 }
 
-// Workgroups, and so rows of partial sums of dw: one per CU where a wave holds
-// a row, two per CU where a workgroup does.
+// Workgroups, and so rows of partial sums of dw.
 int64_t norm_grad_partials(int64_t rows, int64_t cols, int src) {
-  if (cols > kMaxCols) return rows < 64 ? rows : 64;
-  if (grad_by_wave(rows, cols, src)) return 256;
-  return rows < 512 ? rows : 512;
+  if (cols > grad_max_cols(src)) return rows < 64 ? rows : 64;
+  const int64_t per = (WG / 64) / grad_waves(cols), n = (rows + per - 1) / per;
+  return n < 256 ? n : 256;
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {

@@ -5,16 +5,21 @@
 // A weight times its scale is exact in bf16 (two significant bits times a power
 // of two), so the products are exact and the sums run in fp32.
 //
-// Bound: HBM, 17 bytes for 32 weights that are each used once per token.  A
-// workgroup owns 16 rows of W and all of K: its waves take K in steps of 512
-// (4 KB of weights), their partial sums meet in LDS, and nothing is left to
-// join across workgroups, so results do not depend on timing.  The weights are
-// the 16-row operand of a 16x16x32 bf16 matrix instruction and the tokens its
-// 16 columns: one token costs no more weight bytes or conversions than 16.  A
-// lane (row l % 16, group g = l / 16) loads 16 bytes, the whole block 4 i + g of
-// four, and feeds its elements 8 j .. 8 j + 7 to instruction j; the tokens' lanes
-// take the same elements of x, which is all the order that a sum over k needs.
-#include <cstdlib>
+// Bound: HBM, 17 bytes for 32 weights that are each used once per token; for 16
+// tokens and more also the reading of x by each workgroup.  A workgroup owns 16 R
+// rows of W and all of K: its waves take a run of K each, in steps of 128 NI
+// elements, their partial sums meet in LDS, and nothing is left to join across
+// workgroups, so results do not depend on timing.  The weights are the 16-row
+// operand of a 16x16x32 bf16 matrix instruction and the tokens its 16 columns: one
+// token costs no more weight bytes or conversions than 16.  A lane (row l % 16,
+// group g = l / 16) takes the whole block 4 i + g of four and feeds its elements
+// 8 j .. 8 j + 7 to instruction j; the tokens' lanes take the same elements of x,
+// which is all the order that a sum over k needs.
+//
+// Weights and x go through LDS, each wave's own piece, without a barrier: loads from
+// memory then take whole runs of a row.  With operands loaded in their own order
+// (16 bytes of x 64 bytes apart) 4 x 14336 x 4096 took 13.3 us instead of 8.3 (31 MB:
+// 3.8 TB/s), 16 x 4096 x 14336 18.5 instead of 11.9.
 #include "mx_device.hpp"
 #include "mx_layer.h"
 
@@ -26,7 +31,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int ROWS = 16;    // rows of W per workgroup
 
 // Eight E2M1 codes (a dword) times the scale as a bf16 operand.
 __device__ __forceinline__ bf16x8 fp4_operand(uint32_t q, float scale) {
@@ -38,21 +42,11 @@ __device__ __forceinline__ bf16x8 fp4_operand(uint32_t q, float scale) {
   return u.v;
 }
 
-// What a lane takes in one step of NI * 128 elements of K: block 4 i + g of its
-// row of W at q[i], the block's scale at byte g of s[i], and the block's elements
-// of its tokens at x[i][j][t].
-template <int MT, int NI>
-struct Step {
-  uint4 q[NI];
-  uint32_t s[NI];
-  bf16x8 x[NI][4][MT];
-};
-
 // x[k .. k + 7] of a token, +0 past K; rows of x need no alignment beyond their
 // type's.
 template <bool WHOLE>
-__device__ __forceinline__ bf16x8 load_x(const uint16_t* xrow, int64_t k, int64_t K) {
-  union { uint16_t h[8]; bf16x8 v; uint4 u; } r;
+__device__ __forceinline__ uint4 load_x(const uint16_t* xrow, int64_t k, int64_t K) {
+  union { uint16_t h[8]; uint4 u; } r;
   if (WHOLE || k + 8 <= K) {
     __builtin_memcpy(&r.u, xrow + k, 16);
   } else {
@@ -61,130 +55,271 @@ __device__ __forceinline__ bf16x8 load_x(const uint16_t* xrow, int64_t k, int64_
     for (int e = 0; e < 8; e++)
       if (k + e < K) r.h[e] = xrow[k + e];
   }
-  return r.v;
+  return r.u;
 }
 
-// Blocks at or past nb read as zeros.
-template <int MT, int NI, bool WHOLE>
-__device__ __forceinline__ void load_step(Step<MT, NI>& st, const uint8_t* qrow, const uint8_t* srow,
-                                          const uint16_t* const xrow[MT], int b0, int g, int nb, int64_t K) {
+// x[k .. k + 7] of a token, +0 past K; rows of x need no alignment beyond their
+// type's.
+__device__ __forceinline__ uint4 load_x(const uint16_t* xrow, int64_t k, int64_t K) {
+  union { uint16_t h[8]; uint4 u; } r;
+  r.u = make_uint4(0, 0, 0, 0);
+  if (k + 8 <= K) __builtin_memcpy(&r.u, xrow + k, 16);
+  return r.u;
+}
+__device__ __forceinline__ void load_x_tail(const uint16_t* xrow, int64_t k, int64_t K, uint4& x) {
+  if (k >= K || k + 8 <= K) return;
+  union { uint16_t h[8]; uint4 u; } r;
+  r.u = make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int i = 0; i < NI; i++) {
-    const int b = b0 + 4 * i + g;
-    if (WHOLE || b < nb) st.q[i] = *(const uint4*)(qrow + (int64_t)b * 16);
-    else st.q[i] = make_uint4(0, 0, 0, 0);
+  for (int e = 0; e < 8; e++)
+    if (k + e < K) r.h[e] = xrow[k + e];
+  x = r.u;
+}
+
+// One wave's piece of LDS, and what a lane loads for it in a step of 128 NI elements
+// of K.  All loads take whole runs of a row, 64 NI bytes of weights and 256 NI of x.
+template <int TOK, int NI, int R>
+struct Step {
+  static constexpr int ROWS = 16 * R;
+  static constexpr int Q_PITCH = 64 * NI + 16, X_PITCH = 256 * NI + 16, S_PITCH = 64 + 16;  // other banks for each row
+  static constexpr int Q_AT = 0, S_AT = Q_AT + ROWS * Q_PITCH, X_AT = S_AT + ROWS * S_PITCH;
+  static constexpr int BYTES = X_AT + TOK * X_PITCH;
+  static constexpr int XL = (TOK * NI + 3) / 4;
+  static constexpr int SCALED = 64 / (4 * NI);  // steps that one load of scales serves
+  uint4 q[R * NI];
+  uint4 x[XL];
+};
+
+struct Rows {
+  const uint8_t* q;  // first row of the workgroup
+  const uint8_t* s;
+  const uint16_t* x;  // first token
+  int64_t ld_x, K;
+  int nb, rows, live;  // rows and tokens that there are
+};
+
+// Blocks at or past `end` read as zeros; rows and tokens past the last as the last.
+template <int TOK, int NI, int R>
+__device__ __forceinline__ void load_weights(Step<TOK, NI, R>& st, const Rows& w, int b0, int end) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int r = 0; r < R * NI; r++) {
+    const int f = 64 * r + lane, row = f / (4 * NI), b = b0 + f % (4 * NI);
+    st.q[r] = make_uint4(0, 0, 0, 0);
+    if (b < end) st.q[r] = *(const uint4*)(w.q + ((int64_t)(row < w.rows ? row : w.rows - 1) * w.nb + b) * 16);
   }
-  if (WHOLE) {
-    __builtin_memcpy(st.s, srow + b0, 4 * NI);  // any alignment: rows of scales are nb bytes
-  } else {
+}
+template <int TOK, int NI, int R>
+__device__ __forceinline__ void load_tokens(Step<TOK, NI, R>& st, const Rows& w, int b0) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i < NI; i++) {
-      const int b = b0 + 4 * i + g;
-      st.s[i] = b < nb ? (uint32_t)srow[b] << (8 * g) : 0u;
+  for (int r = 0; r < Step<TOK, NI, R>::XL; r++) {
+    const int f = 64 * r + lane, tok = f / (16 * NI);
+    st.x[r] = load_x(w.x + (tok < w.live ? tok : w.live - 1) * w.ld_x, (int64_t)b0 * 32 + 8 * (f % (16 * NI)), w.K);
+  }
+  if ((w.K & 7) && (int64_t)(b0 + 4 * NI) * 32 > w.K) {
+#pragma unroll
+    for (int r = 0; r < Step<TOK, NI, R>::XL; r++) {
+      const int f = 64 * r + lane, tok = f / (16 * NI);
+      load_x_tail(w.x + (tok < w.live ? tok : w.live - 1) * w.ld_x, (int64_t)b0 * 32 + 8 * (f % (16 * NI)), w.K,
+                  st.x[r]);
     }
   }
+}
+// scales of the 64 blocks from b0 on, four lanes a row
+template <int TOK, int NI, int R>
+__device__ __forceinline__ void load_scales(uint4 (&s)[R], const Rows& w, int b0) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < NI; i++)
+  for (int a = 0; a < R; a++) {
+    const int row = 16 * a + lane / 4, b = b0 + 16 * (lane & 3);
+    const uint8_t* src = w.s + (int64_t)(row < w.rows ? row : w.rows - 1) * w.nb + b;
+    union { uint8_t c[16]; uint4 u; } t;
+    t.u = make_uint4(0, 0, 0, 0);
+    if (b + 16 <= w.nb) {
+      __builtin_memcpy(&t.u, src, 16);  // any alignment: rows of scales are nb bytes
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+      for (int e = 0; e < 16; e++)
+        if (b + e < w.nb) t.c[e] = src[e];
+    }
+    s[a] = t.u;
+  }
+}
+template <int TOK, int NI, int R>
+__device__ __forceinline__ void stage_weights(const Step<TOK, NI, R>& st, uint8_t* lds) {
+  using St = Step<TOK, NI, R>;
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-      for (int t = 0; t < MT; t++)
-        st.x[i][j][t] = load_x<WHOLE>(xrow[t], (int64_t)(b0 + 4 * i + g) * 32 + 8 * j, K);
+  for (int r = 0; r < R * NI; r++) {
+    const int f = 64 * r + lane;
+    *(uint4*)(lds + St::Q_AT + f / (4 * NI) * St::Q_PITCH + f % (4 * NI) * 16) = st.q[r];
+  }
+}
+template <int TOK, int NI, int R>
+__device__ __forceinline__ void stage_tokens(const Step<TOK, NI, R>& st, uint8_t* lds) {
+  using St = Step<TOK, NI, R>;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int r = 0; r < St::XL; r++) {
+    const int f = 64 * r + lane;
+    if (TOK * NI < 4 && f >= 16 * NI * TOK) break;  // fewer lanes hold a piece
+    *(uint4*)(lds + St::X_AT + f / (16 * NI) * St::X_PITCH + f % (16 * NI) * 16) = st.x[r];
+  }
+}
+template <int TOK, int NI, int R>
+__device__ __forceinline__ void stage_scales(const uint4 (&s)[R], uint8_t* lds) {
+  using St = Step<TOK, NI, R>;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int a = 0; a < R; a++) *(uint4*)(lds + St::S_AT + (16 * a + lane / 4) * St::S_PITCH + 16 * (lane & 3)) = s[a];
+}
+// lanes of one wave: what one wrote to LDS, the others read
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <int MT, int NI>
-__device__ __forceinline__ void take_step(const Step<MT, NI>& st, int g, f32x4 acc[MT]) {
+// Step `at` of those that the staged scales serve.
+template <int TOK, int NI, int R>
+__device__ __forceinline__ void take_step(const uint8_t* lds, int at, f32x4 (&acc)[R][(TOK + 15) / 16]) {
+  using St = Step<TOK, NI, R>;
+  constexpr int MT = (TOK + 15) / 16;
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int i = 0; i < NI; i++) {
-    const uint32_t code = (st.s[i] >> (8 * g)) & 0xFFu;
-    const float scale = __builtin_bit_cast(float, code << 23);
-    const uint32_t w[4] = {st.q[i].x, st.q[i].y, st.q[i].z, st.q[i].w};
+    uint4 q[R];
+    float scale[R];
+#pragma unroll
+    for (int a = 0; a < R; a++) {
+      q[a] = *(const uint4*)(lds + St::Q_AT + (16 * a + m) * St::Q_PITCH + (4 * i + g) * 16);
+      const uint32_t code = lds[St::S_AT + (16 * a + m) * St::S_PITCH + 4 * NI * at + 4 * i + g];
+      scale[a] = __builtin_bit_cast(float, code << 23);
+    }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const bf16x8 a = fp4_operand(w[j], scale);
+      bf16x8 b[MT];
 #pragma unroll
-      for (int t = 0; t < MT; t++)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, st.x[i][j][t], acc[t], 0, 0, 0);
+      for (int t = 0; t < MT; t++) {
+        const int tok = (16 * t + m) & (TOK - 1);  // columns past TOK repeat the first ones
+        b[t] = *(const bf16x8*)(lds + St::X_AT + tok * St::X_PITCH + (4 * i + g) * 64 + 16 * j);
+      }
+#pragma unroll
+      for (int a = 0; a < R; a++) {
+        const bf16x8 w = fp4_operand(j == 0 ? q[a].x : j == 1 ? q[a].y : j == 2 ? q[a].z : q[a].w, scale[a]);
+#pragma unroll
+        for (int t = 0; t < MT; t++)
+          acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b[t], acc[a][t], 0, 0, 0);
+      }
     }
   }
 }
 
-template <int MT, int NI, int WAVES, int OCC, bool BF16>
-__global__ __launch_bounds__(64 * WAVES, OCC) void k_gemv(GemvArgs p) {
-  __shared__ float part[WAVES][MT][16][ROWS + 1];
+// TOK tokens (1, 2, 4, 8, 16 or 32) and 16 R rows of W by one workgroup.
+template <int TOK, int NI, int WAVES, int R, bool BF16>
+__global__ __launch_bounds__(64 * WAVES) void k_gemv(GemvArgs p) {
+  using St = Step<TOK, NI, R>;
+  constexpr int MT = (TOK + 15) / 16, ROWS = 16 * R;
+  constexpr int PART = 4 * MT * 16 * (ROWS + 1);  // bytes of a wave's partial sums
+  __shared__ __align__(16) uint8_t lds[WAVES * (St::BYTES > PART ? St::BYTES : PART)];
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * ROWS, m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int nb = (int)((p.K + 31) >> 5);
-  // rows past N read row N - 1 again and are not stored
-  const int64_t n = n0 + (lane & 15) < p.N ? n0 + (lane & 15) : p.N - 1;
-  const uint8_t* qrow = p.wq + n * nb * 16;
-  const uint8_t* srow = p.ws + n * nb;
-  const uint16_t* xrow[MT];
-  f32x4 acc[MT];
+  const int64_t n0 = (int64_t)blockIdx.x * ROWS, m0 = (int64_t)blockIdx.y * TOK;
+  Rows w;
+  w.nb = (int)((p.K + 31) >> 5);
+  w.K = p.K;
+  w.q = p.wq + n0 * w.nb * 16;
+  w.s = p.ws + n0 * w.nb;
+  w.x = p.x + m0 * p.ld_x;
+  w.ld_x = p.ld_x;
+  w.rows = p.N - n0 < ROWS ? (int)(p.N - n0) : ROWS;
+  w.live = p.M - m0 < TOK ? (int)(p.M - m0) : TOK;
+  const int live = w.live;
+  f32x4 acc[R][MT];
 #pragma unroll
-  for (int t = 0; t < MT; t++) {  // tokens past M read the first token's row and are not stored
-    const int64_t m = m0 + 16 * t + (lane & 15);
-    xrow[t] = p.x + (m < p.M ? m : m0) * p.ld_x;
-    acc[t] = f32x4{0, 0, 0, 0};
-  }
-  constexpr int STEP = 4 * NI;                 // blocks a wave takes at a time
-  const int whole = (int)(p.K / (32 * STEP));  // steps with all of their blocks and elements
-  int s = wave;
-  for (; s < whole; s += WAVES) {
-    Step<MT, NI> st;
-    load_step<MT, NI, true>(st, qrow, srow, xrow, s * STEP, g, nb, p.K);
-    take_step<MT, NI>(st, g, acc);
-  }
-  if (s == whole && whole * STEP < nb) {  // the short last step
-    Step<MT, NI> st;
-    load_step<MT, NI, false>(st, qrow, srow, xrow, s * STEP, g, nb, p.K);
-    take_step<MT, NI>(st, g, acc);
-  }
-  // lane (g, m) holds rows 4 g .. 4 g + 3 of token m
+  for (int a = 0; a < R; a++)
 #pragma unroll
-  for (int t = 0; t < MT; t++)
-#pragma unroll
-    for (int r = 0; r < 4; r++) part[wave][t][lane & 15][4 * g + r] = acc[t][r];
+    for (int t = 0; t < MT; t++) acc[a][t] = f32x4{0, 0, 0, 0};
+  uint8_t* mine = lds + wave * St::BYTES;
+  constexpr int STEP = 4 * NI;  // blocks a wave takes at a time
+  const int steps = (w.nb + STEP - 1) / STEP, per = (steps + WAVES - 1) / WAVES;
+  int s = wave * per;
+  const int end = s + per < steps ? s + per : steps;
+  if (s < end) {
+    const int last = end * STEP < w.nb ? end * STEP : w.nb;
+    St st;
+    uint4 sc[R];
+    load_scales<TOK, NI, R>(sc, w, s * STEP);
+    load_tokens<TOK, NI, R>(st, w, s * STEP);
+    load_weights<TOK, NI, R>(st, w, s * STEP, last);
+    stage_scales<TOK, NI, R>(sc, mine);
+    for (int at = 0;;) {
+      stage_weights<TOK, NI, R>(st, mine);
+      stage_tokens<TOK, NI, R>(st, mine);
+      wave_fence();
+      s++;
+      if (s < end) {
+        load_tokens<TOK, NI, R>(st, w, s * STEP);
+        load_weights<TOK, NI, R>(st, w, s * STEP, last);
+        if (at == St::SCALED - 1) load_scales<TOK, NI, R>(sc, w, s * STEP);
+      }
+      take_step<TOK, NI, R>(mine, at, acc);
+      wave_fence();
+      if (s >= end) break;
+      if (++at == St::SCALED) {
+        stage_scales<TOK, NI, R>(sc, mine);
+        at = 0;
+      }
+    }
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 256 * MT; i += 64 * WAVES) {
-    const int t = i >> 8, m = (i >> 4) & 15, r = i & 15;
-    if (m0 + 16 * t + m >= p.M || n0 + r >= p.N) continue;
+  // lane (g, m) holds rows 4 g .. 4 g + 3 of token m
+  float* part = (float*)lds;
+  auto at = [](int w, int m, int r) { return (w * MT * 16 + m) * (ROWS + 1) + r; };
+#pragma unroll
+  for (int a = 0; a < R; a++)
+#pragma unroll
+    for (int t = 0; t < MT; t++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) part[at(wave, 16 * t + (lane & 15), 16 * a + 4 * g + r)] = acc[a][t][r];
+  __syncthreads();
+  for (int i = threadIdx.x; i < TOK * ROWS; i += 64 * WAVES) {
+    const int m = i / ROWS, r = i % ROWS;
+    if (m >= live || n0 + r >= p.N) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; w++) v += part[w][t][m][r];
-    const int64_t at = (m0 + 16 * t + m) * p.ld_y + n0 + r;
-    if (BF16) ((uint16_t*)p.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
-    else ((float*)p.y)[at] = v;
+    for (int w = 0; w < WAVES; w++) v += part[at(w, m, r)];
+    const int64_t to = (m0 + m) * p.ld_y + n0 + r;
+    if (BF16) ((uint16_t*)p.y)[to] = __builtin_bit_cast(uint16_t, (__bf16)v);
+    else ((float*)p.y)[to] = v;
   }
+}
+
+template <int TOK, int NI, int WAVES, int R>
+void go(const GemvArgs& a, hipStream_t st) {
+  const dim3 g((unsigned)((a.N + 16 * R - 1) / (16 * R)), (unsigned)((a.M + TOK - 1) / TOK)), b(64 * WAVES);
+  if (a.bf16) hipLaunchKernelGGL((k_gemv<TOK, NI, WAVES, R, true>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((k_gemv<TOK, NI, WAVES, R, false>), g, b, 0, st, a);
 }
 
 }  // namespace
 
-template <int MT, int NI, int W, int OCC>
-static void go(const GemvArgs& a, dim3 g, hipStream_t st) {
-  if (a.bf16) hipLaunchKernelGGL((k_gemv<MT, NI, W, OCC, true>), g, dim3(64 * W), 0, st, a);
-  else hipLaunchKernelGGL((k_gemv<MT, NI, W, OCC, false>), g, dim3(64 * W), 0, st, a);
-}
+// Where 16-row groups are fewer than two for each of the 256 CUs, eight waves share
+// a group's K; where there are more, four do, so that more workgroups fit on a CU,
+// and for many tokens a workgroup takes several groups, since each group reads all
+// of x.  Measured (us, eight waves and one group / the other form):
+//   1 x 4096 x 14336   7.9 / 10.6     1 x 14336 x 4096    8.1 / 7.7
+//   4 x 14336 x 4096   9.2 / 8.3      16 x 14336 x 4096  17.9 / 11.1 (two groups)
+//   16 x 4096 x 14336 11.9 / 19.3     32 x 14336 x 14336 71.0 / 45.0 (four groups)
 hipError_t launch_gemv(const GemvArgs& a, hipStream_t st) {
-  const unsigned gx = (unsigned)((a.N + ROWS - 1) / ROWS);
-  static const int V = getenv("MXV") ? atoi(getenv("MXV")) : 0;
-  if (a.M <= 16) {
-    const dim3 g(gx, 1);
-    switch (V) {
-      case 0: go<1, 4, 8, 4>(a, g, st); break;
-      case 1: go<1, 2, 8, 4>(a, g, st); break;
-      case 2: go<1, 2, 8, 8>(a, g, st); break;
-      case 3: go<1, 4, 16, 4>(a, g, st); break;
-      case 4: go<1, 2, 16, 8>(a, g, st); break;
-      case 5: go<1, 2, 16, 4>(a, g, st); break;
-      case 6: go<1, 4, 4, 4>(a, g, st); break;
-      case 7: go<1, 2, 4, 8>(a, g, st); break;
-    }
-  } else {  // each 32 tokens read the weights once
-    const dim3 g(gx, (unsigned)((a.M + 31) / 32));
-    go<2, 2, 8, 4>(a, g, st);
-  }
+  const bool many = (a.N + 15) / 16 > 512;
+  if (a.M == 1) many ? go<1, 2, 4, 1>(a, st) : go<1, 2, 8, 1>(a, st);
+  else if (a.M == 2) many ? go<2, 2, 4, 1>(a, st) : go<2, 2, 8, 1>(a, st);
+  else if (a.M <= 4) many ? go<4, 2, 4, 1>(a, st) : go<4, 2, 8, 1>(a, st);
+  else if (a.M <= 8) many ? go<8, 2, 4, 1>(a, st) : go<8, 2, 8, 1>(a, st);
+  else if (a.M <= 16) many ? go<16, 2, 4, 2>(a, st) : go<16, 2, 8, 1>(a, st);
+  else many ? go<32, 1, 4, 4>(a, st) : go<32, 1, 8, 1>(a, st);  // 32 tokens a reading of the weights
   return hipGetLastError();
 }
 

@@ -61,27 +61,32 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p) {
 // attention
 // ---------------------------------------------------------------------------
 // Rows of a key/value head are its (query token, query head) pairs; a workgroup
-// takes NR tiles of 16 of them and one piece of the request's tokens, its four
-// waves 32 tokens at a time.  Both products run on 16x16x32 bf16 matrix
-// instructions, to which an element times its scale is exact, straight from
-// registers:
-//   S^T = K Q^T   lane (l % 16, g = l / 16) loads dims g D/4 .. of token l % 16
-//                 and feeds dims 8 j .. of them to instruction j, as the lane of
-//                 Q does; it gets rows' scores of tokens 4 g .. 4 g + 3
-//   O^T = V^T P^T those 8 scores (two groups of 16 tokens) are the lane's 8 of
-//                 the 32 of a sum over tokens as they are; the lane loads dims
+// takes NR tiles of 16 of them and one piece of the request's tokens, each wave 32
+// tokens at a time.  Both products run on 16x16x32 bf16 matrix instructions, to
+// which an element times its scale is exact:
+//   S^T = K Q^T   lane (l % 16, g = l / 16) takes dims g D/4 .. of token l % 16 and
+//                 feeds dims 8 j .. of them to instruction j, as the lane of Q does;
+//                 it gets its row's scores of tokens 4 g .. 4 g + 3
+//   O^T = V^T P^T those 8 scores (two groups of 16 tokens) are the lane's 8 of the
+//                 32 of a sum over tokens as they are; the lane takes dims
 //                 (l % 16) D/16 .. of the same 8 tokens and transposes 2 x 2
-// so neither P nor V passes through LDS.  P is rounded to bf16 (relative error
-// 2^-9, of the size of the output's own rounding); scores, maxima, sums and O
-// stay in fp32.
-constexpr int WAVES = 4;
+// so P stays in registers.  P is rounded to bf16 (relative error 2^-9, of the size of
+// the output's own rounding); scores, maxima, sums and O stay in fp32.
+//
+// Bound for a few rows: HBM, 2 (D + D / 32) bytes a token and head.  Each wave loads
+// its 32 tokens in whole 1 KB runs and reads them again from its own piece of LDS:
+// with loads in the operands' order (16 bytes of a token 32 bytes apart, scales byte
+// by byte) 32 requests to 16384 took 165 us, 136 us now (4.9 TB/s).  The next 32
+// tokens are in flight meanwhile.
+struct u64x2 { uint2 lo, hi; };
+
 constexpr int STEP = 32;  // tokens a wave takes at a time
 
 struct AttnArgs {
   AttentionArgs a;
   int rows;              // Lq * group
   int splits;
-  int chunk;             // tokens of a piece, a multiple of STEP * WAVES
+  int chunk;             // tokens of a piece, a multiple of what its waves take at a time
   uint32_t page16, magic;  // page / 16 and the constant that divides by it
   float* part_o;         // [B][heads][rows][splits][dim]
   float* part_ml;        // [B][heads][rows][splits][2]
@@ -119,13 +124,21 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {  // 
   }
 }
 
-// The bytes of 32 tokens in a lane.
+// The bytes of 32 tokens in a lane: in 16-byte pieces of each group of 16 tokens in
+// the order of the cache, and the scales of token l % 16, keys of the first and of
+// the second group, then values.
 template <int D>
 struct Raw {
-  uint32_t k[2][D / 16];     // dims g D/4 .. of token 16 u + l % 16
-  uint32_t ks[2];            // the scales of those dims (one, or two for 256)
-  uint32_t v[2][4][D / 64];  // dims (l % 16) D/16 .. of token 16 u + 4 g + r
-  uint32_t vs[2][D / 32];    // the scales of tokens 16 u + 4 g .. + 3, D / 32 bytes each
+  u32x4 k[2][D / 64], v[2][D / 64];
+  uint32_t s[D == 256 ? 2 : 1];
+};
+// A wave's piece of LDS: rows of keys, of values and of scales, with pitches that
+// spread the lanes' reads over the banks.
+template <int D>
+struct Stage {
+  static constexpr int KP = D + 16, VP = D == 128 ? 160 : D + 16, SP = D / 32;
+  static constexpr int K_AT = 0, V_AT = K_AT + 32 * KP, KS_AT = V_AT + 32 * VP, VS_AT = KS_AT + 32 * SP;
+  static constexpr int BYTES = VS_AT + 32 * SP;
 };
 
 // Where tokens 16 u .. of a request lie: row (page, head, place) of the cache.
@@ -138,32 +151,83 @@ __device__ __forceinline__ bool locate(const AttnArgs& p, const int32_t* table, 
   return (uint32_t)pg < (uint32_t)p.a.c.pages;
 }
 
-// Rows are the same for the whole wave, so addresses are a scalar base and a
-// lane's constant offset.
 template <int D>
 __device__ __forceinline__ uint32_t load_step(const AttnArgs& p, const int32_t* table, int head, int t0, int end,
                                               Raw<D>& x) {
-  const uint32_t lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63;
   uint32_t there = 0;
+  int64_t row[2];
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    int64_t row = 0;
     bool ok = t0 + 16 * u < end;
-    if (ok) ok = locate(p, table, head, t0 + 16 * u, row);
-    if (!ok) row = 0;  // any row of the cache: what it holds is masked
+    if (ok) ok = locate(p, table, head, t0 + 16 * u, row[u]);
+    if (!ok) row[u] = 0;  // any row of the cache: what it holds is masked
     there |= (uint32_t)ok << u;
-    const uint8_t* kq = p.a.c.k_q + row * D;
-    const uint8_t* ks = p.a.c.k_s + row * (D / 32);
-    const uint8_t* vq = p.a.c.v_q + row * D;
-    const uint8_t* vs = p.a.c.v_s + row * (D / 32);
-    load_words<D / 16>(kq + (i * D + g * (D / 4)), x.k[u]);
-    if constexpr (D == 256) x.ks[u] = *(const uint16_t*)(ks + (i * 8 + 2 * g));
-    else x.ks[u] = ks[i * (D / 32) + g * D / 128];
-#pragma unroll
-    for (int r = 0; r < 4; r++) load_words<D / 64>(vq + (4 * g * D + i * (D / 16)) + r * D, x.v[u][r]);
-    load_words<D / 32>(vs + 4 * g * (D / 32), x.vs[u]);
   }
+#pragma unroll
+  for (int u = 0; u < 2; u++)
+#pragma unroll
+    for (int c = 0; c < D / 64; c++) {
+      x.k[u][c] = *(const u32x4*)(p.a.c.k_q + row[u] * D + (1024 * c + 16 * lane));
+      x.v[u][c] = *(const u32x4*)(p.a.c.v_q + row[u] * D + (1024 * c + 16 * lane));
+    }
+  const uint8_t* s = (lane & 32 ? p.a.c.v_s : p.a.c.k_s) + ((lane & 16 ? row[1] : row[0]) + (lane & 15)) * (D / 32);
+  if constexpr (D == 64) x.s[0] = *(const uint16_t*)s;
+  else load_words<D / 128>(s, x.s);
   return there;
+}
+
+// Into the wave's piece of LDS.  `cut`: tokens at or past `end` or not there may be
+// among them; they count as zeros whatever the cache holds there, for 0 * NaN is
+// not 0.  True where a value of the others may not be finite (asked only then).
+template <int D, int F>
+__device__ __forceinline__ bool stage_step(Raw<D>& x, uint8_t* lds, bool cut, uint32_t there, int end) {
+  using St = Stage<D>;
+  const int lane = threadIdx.x & 63;
+  bool odd = false;
+  if (cut) {
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int c = 0; c < D / 64; c++) {
+        const int tok = 16 * u + (64 * c + lane) / (D / 16);
+        const bool gone = !(there >> u & 1) || tok >= end;
+        const u32x4 v = gone ? u32x4{0, 0, 0, 0} : x.v[u][c];
+        x.v[u][c] = v;
+        constexpr uint32_t add = F == E4M3 ? 0x01010101u : 0x04040404u;  // to the sign bit: NaN, or Inf and NaN
+        odd |= ((((v.x & 0x7F7F7F7Fu) + add) | ((v.y & 0x7F7F7F7Fu) + add) | ((v.z & 0x7F7F7F7Fu) + add) |
+                 ((v.w & 0x7F7F7F7Fu) + add)) & 0x80808080u) != 0;
+      }
+    if (lane & 32) {
+      const int u = (lane >> 4) & 1;
+      const bool gone = !(there >> u & 1) || 16 * u + (lane & 15) >= end;
+#pragma unroll
+      for (int c = 0; c < (D == 256 ? 2 : 1); c++) {
+        if (gone) x.s[c] = 0x7F7F7F7Fu;
+#pragma unroll
+        for (int k = 0; k < (D == 64 ? 2 : 4); k++) odd |= ((x.s[c] >> (8 * k)) & 0xFFu) > (uint32_t)(254 - Fmt<F>::emax);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 2; u++)
+#pragma unroll
+    for (int c = 0; c < D / 64; c++) {
+      const int f = 64 * c + lane, tok = 16 * u + f / (D / 16), at = f % (D / 16) * 16;
+      *(u32x4*)(lds + St::K_AT + tok * St::KP + at) = x.k[u][c];
+      *(u32x4*)(lds + St::V_AT + tok * St::VP + at) = x.v[u][c];
+    }
+  uint8_t* s = lds + St::KS_AT + lane * St::SP;  // keys 0 .. 31, values 0 .. 31
+  if constexpr (D == 64) *(uint16_t*)s = (uint16_t)x.s[0];
+  else if constexpr (D == 128) *(uint32_t*)s = x.s[0];
+  else *(uint2*)s = make_uint2(x.s[0], x.s[1]);
+  return odd;
+}
+// lanes of one wave: what one wrote to LDS, the others read
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 __device__ __forceinline__ bf16x8 operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -173,27 +237,26 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-// Scale code of the lane's dims of V for token 16 u + 4 g + r: byte r D/32 +
-// block of x.vs[u].
-template <int D>
-__device__ __forceinline__ uint32_t v_scale(const Raw<D>& x, int u, int r) {
-  const int blk = (int)(threadIdx.x & 15) * (D / 16) / 32;
-  if constexpr (D == 64) return (x.vs[u][r >> 1] >> (16 * (r & 1) + 8 * blk)) & 0xFFu;
-  else if constexpr (D == 128) return (x.vs[u][r] >> (8 * blk)) & 0xFFu;
-  else return ((blk & 4 ? x.vs[u][2 * r + 1] : x.vs[u][2 * r]) >> (8 * (blk & 3))) & 0xFFu;
-}
-
 // V as operands of the second product: dims (l % 16) D/16 + 4 k .. + 3 of the
-// lane's 8 tokens (dword c of an operand: tokens 2 c and 2 c + 1 of the eight).
+// lane's 8 tokens, 16 u + 4 g + r (dword c of an operand: tokens 2 c and 2 c + 1).
 template <int D, int F>
-__device__ __forceinline__ void v_operands(const Raw<D>& x, const float s[2][4], int k, uint32_t w[4][4]) {
+__device__ __forceinline__ void v_operands(const uint8_t* lds, int k, uint32_t (&w)[4][4]) {
+  using St = Stage<D>;
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int u = 0; u < 2; u++)
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      const uint32_t ra = x.v[u][2 * h][k], rb = x.v[u][2 * h + 1][k];
-      const uint32_t a0 = cvt_lo<F>(ra, s[u][2 * h]), a1 = cvt_hi<F>(ra, s[u][2 * h]);
-      const uint32_t b0 = cvt_lo<F>(rb, s[u][2 * h + 1]), b1 = cvt_hi<F>(rb, s[u][2 * h + 1]);
+      uint32_t raw[2];
+      float s[2];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const int tok = 16 * u + 4 * g + 2 * h + e;
+        raw[e] = *(const uint32_t*)(lds + St::V_AT + tok * St::VP + i * (D / 16) + 4 * k);
+        s[e] = e8m0(lds[St::VS_AT + tok * St::SP + i * (D / 16) / 32]);
+      }
+      const uint32_t a0 = cvt_lo<F>(raw[0], s[0]), a1 = cvt_hi<F>(raw[0], s[0]);
+      const uint32_t b0 = cvt_lo<F>(raw[1], s[1]), b1 = cvt_hi<F>(raw[1], s[1]);
       w[0][2 * u + h] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
       w[1][2 * u + h] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
       w[2][2 * u + h] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
@@ -208,30 +271,43 @@ struct Sums {
   float m[NR], l[NR];   // l over the lane's tokens only
 };
 
-// One step of 32 tokens.  `cut`: some row does not see all of them, or some are
-// not there.  limit[n] is the number of them that the lane's row sees (less than
-// 1: none, 32 or more: all), `end` the largest such number of the workgroup.
+// One step of 32 staged tokens.  `cut`: some row does not see all of them, or some
+// are not there.  limit[n] is the number of them that the lane's row sees (less than
+// 1: none, 32 or more: all).  `odd`: values may not be finite and rows see different
+// tokens.
 template <int D, int F, int NR>
-__device__ __forceinline__ void take_step(const AttnArgs& p, Raw<D>& x, const bf16x8 (&q)[NR][D / 32],
-                                          float scale2, bool cut, uint32_t there, int end,
-                                          const int (&limit)[NR], Sums<D, NR>& sum) {
-  const int g = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[D / 32][64], float scale2, bool cut,
+                                          bool odd, uint32_t there, const int (&limit)[NR], Sums<D, NR>& sum) {
+  using St = Stage<D>;
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
   f32x4 s[NR][2];
 #pragma unroll
-  for (int u = 0; u < 2; u++) {
+  for (int n = 0; n < NR; n++) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int n = 0; n < NR; n++) s[n][u] = f32x4{0, 0, 0, 0};
+  for (int c = 0; c < D / 64; c++) {  // 16 bytes: dims g D/4 + 16 c .. of token 16 u + i
+    uint4 kw[2];
+    float ks[2];
 #pragma unroll
-    for (int j = 0; j < D / 32; j++) {
-      const uint32_t code = D == 256 ? (x.ks[u] >> (8 * (j >> 2))) & 0xFFu : x.ks[u];
-      const float ks = e8m0(code);
-      const uint32_t w0 = x.k[u][2 * j], w1 = x.k[u][2 * j + 1];
-      const bf16x8 k = operand(cvt_lo<F>(w0, ks), cvt_hi<F>(w0, ks), cvt_lo<F>(w1, ks), cvt_hi<F>(w1, ks));
+    for (int u = 0; u < 2; u++) {
+      kw[u] = *(const uint4*)(lds + St::K_AT + (16 * u + i) * St::KP + g * (D / 4) + 16 * c);
+      ks[u] = e8m0(lds[St::KS_AT + (16 * u + i) * St::SP + (g * (D / 4) + 16 * c) / 32]);
+    }
 #pragma unroll
-      for (int n = 0; n < NR; n++) s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[n][j], s[n][u], 0, 0, 0);
+    for (int h = 0; h < 2; h++) {
+      bf16x8 k[2];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const uint32_t w0 = h ? kw[u].z : kw[u].x, w1 = h ? kw[u].w : kw[u].y;
+        k[u] = operand(cvt_lo<F>(w0, ks[u]), cvt_hi<F>(w0, ks[u]), cvt_lo<F>(w1, ks[u]), cvt_hi<F>(w1, ks[u]));
+      }
+#pragma unroll
+      for (int n = 0; n < NR; n++) {
+        const bf16x8 qj = q[n][2 * c + h][threadIdx.x & 63];
+#pragma unroll
+        for (int u = 0; u < 2; u++) s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u], qj, s[n][u], 0, 0, 0);
+      }
     }
   }
-  bool odd = false;
   if (cut) {
 #pragma unroll
     for (int n = 0; n < NR; n++)
@@ -241,33 +317,6 @@ __device__ __forceinline__ void take_step(const AttnArgs& p, Raw<D>& x, const bf
         const bool seen = tok < limit[n] && (there >> (e >> 2) & 1);
         s[n][e >> 2][e & 3] = seen ? s[n][e >> 2][e & 3] : -__builtin_inff();
       }
-    // Tokens that no row sees count as zeros whatever the cache holds there, for
-    // 0 * NaN is not 0.  Of the others, one with a value that may not be finite
-    // sends the step the long way (below) where rows see different tokens.
-#pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-      for (int r = 0; r < 4; r++) {
-        const bool gone = !(there >> u & 1) || 16 * u + 4 * g + r >= end;
-        odd |= !gone && v_scale<D>(x, u, r) > (uint32_t)(254 - Fmt<F>::emax);
-#pragma unroll
-        for (int k = 0; k < D / 64; k++) {
-          x.v[u][r][k] = gone ? 0u : x.v[u][r][k];
-          odd |= (((x.v[u][r][k] & 0x7F7F7F7Fu) + (F == E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u) != 0;
-        }
-      }
-  }
-  float vs[2][4];
-#pragma unroll
-  for (int u = 0; u < 2; u++)
-#pragma unroll
-    for (int r = 0; r < 4; r++) vs[u][r] = e8m0(v_scale<D>(x, u, r));
-  if (cut) {  // a scale of a token that is not there may be a NaN
-#pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-      for (int r = 0; r < 4; r++)
-        vs[u][r] = !(there >> u & 1) || 16 * u + 4 * g + r >= end ? 1.0f : vs[u][r];
   }
   bf16x8 pr[NR];
 #pragma unroll
@@ -294,31 +343,34 @@ __device__ __forceinline__ void take_step(const AttnArgs& p, Raw<D>& x, const bf
     }
     pr[n] = operand(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
   }
-  if (p.a.Lq > 1 && __any(odd)) {
-    // each number of tokens by itself, with the values past it cut, for the rows
-    // that see that many
-    for (int lim = 1; lim <= STEP; lim++) {
-      uint32_t keep[4];
+  if (odd) {
+    // 0 * NaN is not 0: token by token, for the rows that see it.  p takes the
+    // place of the keys.
 #pragma unroll
-      for (int c = 0; c < 4; c++) {
-        const int tok = 16 * (c >> 1) + 4 * g + 2 * (c & 1);
-        keep[c] = (tok < lim ? 0xFFFFu : 0u) | (tok + 1 < lim ? 0xFFFF0000u : 0u);
-      }
+    for (int n = 0; n < NR; n++) {
+      wave_fence();
+      uint16_t* ps = (uint16_t*)(lds + St::K_AT);  // [row][token]
+      *(uint2*)(ps + 32 * i + 4 * g) = __builtin_bit_cast(u64x2, pr[n]).lo;
+      *(uint2*)(ps + 32 * i + 16 + 4 * g) = __builtin_bit_cast(u64x2, pr[n]).hi;
+      wave_fence();
+      for (int tok = 0; tok < STEP; tok++) {
+        if (tok >= limit[n]) continue;
+        const float pt = __builtin_bit_cast(float, (uint32_t)ps[32 * i + tok] << 16);
 #pragma unroll
-      for (int k = 0; k < D / 64; k++) {
-        uint32_t w[4][4];
-        v_operands<D, F>(x, vs, k, w);
+        for (int e = 0; e < 4; e++)
 #pragma unroll
-        for (int d = 0; d < 4; d++) {
-          const bf16x8 v = operand(w[d][0] & keep[0], w[d][1] & keep[1], w[d][2] & keep[2], w[d][3] & keep[3]);
+          for (int k = 0; k < D / 64; k++) {
+            const int at = (4 * g + e) * (D / 16) + 4 * k;  // dims at .. at + 3
+            const uint32_t raw = *(const uint32_t*)(lds + St::V_AT + tok * St::VP + at);
+            const float sc = e8m0(lds[St::VS_AT + tok * St::SP + at / 32]);
+            const uint32_t a = cvt_lo<F>(raw, sc), b = cvt_hi<F>(raw, sc);
 #pragma unroll
-          for (int n = 0; n < NR; n++) {
-            const f32x4 o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[n], sum.o[n][4 * k + d], 0, 0, 0);
-            const bool mine = lim == (limit[n] < STEP ? limit[n] : STEP);
-#pragma unroll
-            for (int e = 0; e < 4; e++) sum.o[n][4 * k + d][e] = mine ? o[e] : sum.o[n][4 * k + d][e];
+            for (int d = 0; d < 4; d++) {
+              const uint32_t h = d < 2 ? a : b;
+              const float v = __builtin_bit_cast(float, d & 1 ? h & 0xFFFF0000u : h << 16);
+              sum.o[n][4 * k + d][e] = __builtin_fmaf(pt, v, sum.o[n][4 * k + d][e]);
+            }
           }
-        }
       }
     }
     return;
@@ -326,7 +378,7 @@ __device__ __forceinline__ void take_step(const AttnArgs& p, Raw<D>& x, const bf
 #pragma unroll
   for (int k = 0; k < D / 64; k++) {
     uint32_t w[4][4];
-    v_operands<D, F>(x, vs, k, w);
+    v_operands<D, F>(lds, k, w);
 #pragma unroll
     for (int d = 0; d < 4; d++) {
       const bf16x8 v = operand(w[d][0], w[d][1], w[d][2], w[d][3]);
@@ -337,10 +389,14 @@ __device__ __forceinline__ void take_step(const AttnArgs& p, Raw<D>& x, const bf
   }
 }
 
-template <int D, int F, int NR>
-__global__ __launch_bounds__(64 * WAVES, D < 256 && NR == 1 ? 2 : 1) void k_attention(AttnArgs p) {
+template <int D, int F, int NR, int WAVES, int OCC>
+__global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
   __shared__ float ml[WAVES][NR][16][2];
-  __shared__ float os[WAVES][16][D + 4];
+  // the waves' staged tokens, then their outputs
+  constexpr int OS = 4 * 16 * (D + 4), PIECE = Stage<D>::BYTES > OS ? Stage<D>::BYTES : OS;
+  __shared__ __align__(16) uint8_t lds[WAVES * PIECE];
+  float(*os)[16][D + 4] = (float(*)[16][D + 4])lds;
+  __shared__ bf16x8 q[NR][D / 32][64];  // by lane, the same for every wave
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x, head = blockIdx.z % p.a.c.heads, b = blockIdx.z / p.a.c.heads;
@@ -362,7 +418,6 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NR == 1 ? 2 : 1) void k_atte
   if (split > 0 && t0 >= t1) return;  // the whole workgroup: no such piece of this request
 
   const int heads_q = p.a.c.heads * p.a.group;
-  bf16x8 q[NR][D / 32];
   Sums<D, NR> sum;
 #pragma unroll
   for (int n = 0; n < NR; n++) {
@@ -370,32 +425,34 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NR == 1 ? 2 : 1) void k_atte
     row = row < p.rows ? row : p.rows - 1;
     const int qt = row / p.a.group, hq = head * p.a.group + row - qt * p.a.group;
     const uint16_t* src = p.a.q + ((int64_t)b * p.a.Lq + qt) * p.a.ld_q + (int64_t)hq * D + g * (D / 4);
-#pragma unroll
-    for (int j = 0; j < D / 32; j++) q[n][j] = *(const bf16x8*)(src + 8 * j);
+    for (int j = wave; j < D / 32; j += WAVES) q[n][j][lane] = *(const bf16x8*)(src + 8 * j);
     sum.m[n] = -__builtin_inff();
     sum.l[n] = 0.0f;
 #pragma unroll
     for (int d = 0; d < D / 16; d++) sum.o[n][d] = f32x4{0, 0, 0, 0};
   }
+  __syncthreads();
   const float scale2 = p.a.scale * 1.44269504088896340736f;  // scores in units of log 2
 
   int t = t0 + wave * STEP;
   if (t < t1) {
+    uint8_t* mine = lds + wave * Stage<D>::BYTES;
     Raw<D> x;
     uint32_t there = load_step<D>(p, table, head, t, t1, x);
     while (true) {
+      const bool cut = there != 3u || t + STEP > low;
+      const uint32_t here = there;
+      const bool odd = __any(stage_step<D, F>(x, mine, cut, here, t1 - t)) && p.a.Lq > 1;
+      wave_fence();
       const int next = t + WAVES * STEP;
-      Raw<D> ahead;
-      uint32_t there_next = 0;
-      if (next < t1) there_next = load_step<D>(p, table, head, next, t1, ahead);
+      if (next < t1) there = load_step<D>(p, table, head, next, t1, x);
       int limit[NR];
 #pragma unroll
       for (int n = 0; n < NR; n++) limit[n] = lim[n] - t;
-      take_step<D, F, NR>(p, x, q, scale2, there != 3u || t + STEP > low, there, t1 - t, limit, sum);
+      take_step<D, F, NR>(mine, q, scale2, cut, odd, here, limit, sum);
+      wave_fence();
       t = next;
       if (t >= t1) break;
-      x = ahead;
-      there = there_next;
     }
   }
 
@@ -454,13 +511,14 @@ __global__ __launch_bounds__(64 * WAVES, D < 256 && NR == 1 ? 2 : 1) void k_atte
   }
 }
 
-// Joins the pieces of a row; one wave a row.
+// Joins the pieces of a row.  A workgroup takes a row, each of its waves every
+// fourth piece; their sums meet in LDS.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_join(AttnArgs p) {
+  __shared__ float part[4][D + 1];
   const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t total = (int64_t)p.a.B * p.a.c.heads * p.rows;
-  if (at >= total) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t at = blockIdx.x;
   const int row = (int)(at % p.rows);
   const int64_t bh = at / p.rows;
   const int head = (int)(bh % p.a.c.heads), b = (int)(bh / p.a.c.heads);
@@ -468,45 +526,64 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs p) {
   len = len < 0 ? 0 : (int64_t)len > p.a.max_len ? (int)p.a.max_len : len;
   const int qt = row / p.a.group, hq = head * p.a.group + row - qt * p.a.group;
   const int limit = len - p.a.Lq + 1 + qt;
-  // the pieces that were computed for this row's tile reach past it or end with it
-  int n = limit <= 0 ? 0 : (limit + p.chunk - 1) / p.chunk;
+  // the pieces that hold tokens of this row; its workgroups have computed them all
+  const int n = limit <= 0 ? 0 : (limit + p.chunk - 1) / p.chunk;
   const float* mls = p.part_ml + 2 * at * p.splits;
   float m = -__builtin_inff();
-  for (int s = 0; s < n; s++) m = __builtin_fmaxf(m, mls[2 * s]);
+  for (int s = lane; s < n; s += 64) m = __builtin_fmaxf(m, mls[2 * s]);
+  m = rows_max(m);
+  m = __builtin_fmaxf(m, dpp<0xB1>(m));
+  m = __builtin_fmaxf(m, dpp<0x4E>(m));
+  m = __builtin_fmaxf(m, dpp<0x141>(m));
+  m = __builtin_fmaxf(m, dpp<0x140>(m));
   const float base = m == -__builtin_inff() ? 0.0f : m;
   float l = 0.0f, o[D / 64] = {};
-  for (int s = 0; s < n; s++) {
+#pragma unroll 4
+  for (int s = wave; s < n; s += 4) {
     const float a = __builtin_amdgcn_exp2f(mls[2 * s] - base);
     l += mls[2 * s + 1] * a;
 #pragma unroll
     for (int k = 0; k < D / 64; k++) o[k] += p.part_o[(at * p.splits + s) * D + 64 * k + lane] * a;
   }
-  const int64_t tok = (int64_t)b * p.a.Lq + qt;
 #pragma unroll
-  for (int k = 0; k < D / 64; k++)
-    p.a.o[tok * p.a.ld_o + (int64_t)hq * D + 64 * k + lane] =
-        __builtin_bit_cast(uint16_t, (__bf16)(l == 0.0f ? 0.0f : o[k] / l));
-  if (lane == 0 && p.a.lse)
+  for (int k = 0; k < D / 64; k++) part[wave][64 * k + lane] = o[k];
+  if (lane == 0) part[wave][D] = l;
+  __syncthreads();
+  l = part[0][D] + part[1][D] + part[2][D] + part[3][D];
+  const int64_t tok = (int64_t)b * p.a.Lq + qt;
+  for (int d = threadIdx.x; d < D; d += 256) {
+    const float v = part[0][d] + part[1][d] + part[2][d] + part[3][d];
+    p.a.o[tok * p.a.ld_o + (int64_t)hq * D + d] = __builtin_bit_cast(uint16_t, (__bf16)(l == 0.0f ? 0.0f : v / l));
+  }
+  if (threadIdx.x == 0 && p.a.lse)
     p.a.lse[tok * (p.a.c.heads * p.a.group) + hq] =
         l == 0.0f ? -__builtin_inff() : m * 0.69314718055994530942f + logf(l);
 }
 
-// Row tiles of a workgroup, and how the tokens are split: by sizes that the
-// host knows, so a result does not depend on timing.
+// Row tiles and waves of a workgroup, and how the tokens are split: by sizes that
+// the host knows, so a result does not depend on timing.
 struct Plan {
-  int nr, tiles, splits, chunk;
+  int nr, waves, tiles, splits, chunk;
 };
+// More tiles share the conversion of the tokens, as far as registers go without
+// spilling (dim 128: two; four ran 60 us against 38 us for 4 requests of 64 query
+// tokens to 4096).  Workgroups are wanted twice for each that the chip holds at a
+// time (two of four waves a CU, one for dim 256), which evens out requests of
+// different lengths: 32 requests to 16384, dim 128, took 136 us in 4 pieces, 143 in
+// 16.  Up to 1024 tokens of few rows eight waves of one workgroup spare the second
+// launch.
 Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_len) {
   Plan r;
   const int64_t rows = Lq * group;
   r.nr = rows <= 16 || dim == 256 ? 1 : rows <= 32 || dim == 128 ? 2 : 4;
+  r.waves = r.nr == 1 && dim < 256 && max_len <= 1024 ? 8 : 4;
   r.tiles = (int)((rows + 16 * r.nr - 1) / (16 * r.nr));
-  const int64_t unit = STEP * WAVES, base = B * heads * r.tiles;
+  const int64_t unit = STEP * r.waves, base = B * heads * r.tiles, want = dim == 256 ? 512 : 1024;
   const int64_t units = (max_len + unit - 1) / unit;
-  int64_t want = (1024 + base - 1) / base;  // four workgroups for each CU
-  if (want > (units + 1) / 2) want = (units + 1) / 2;  // at least two steps a wave
-  if (want < 1) want = 1;
-  int64_t per = (units + want - 1) / want;
+  int64_t splits = r.waves == 8 ? 1 : (want + base - 1) / base;
+  if (splits > (units + 1) / 2) splits = (units + 1) / 2;  // at least two steps a wave
+  if (splits < 1) splits = 1;
+  int64_t per = (units + splits - 1) / splits;
   if (per < 1) per = 1;
   r.chunk = (int)(per * unit);
   r.splits = (int)((units + per - 1) / per);
@@ -516,16 +593,19 @@ Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_l
 
 template <int D, int F>
 hipError_t attention_by_rows(const AttnArgs& p, const Plan& r, hipStream_t st) {
-  const dim3 g((unsigned)r.splits, (unsigned)r.tiles, (unsigned)(p.a.B * p.a.c.heads)), b(64 * WAVES);
-  if (r.nr == 1) hipLaunchKernelGGL((k_attention<D, F, 1>), g, b, 0, st, p);
-  if constexpr (D <= 128)
-    if (r.nr == 2) hipLaunchKernelGGL((k_attention<D, F, 2>), g, b, 0, st, p);
-  if constexpr (D == 64)
-    if (r.nr == 4) hipLaunchKernelGGL((k_attention<D, F, 4>), g, b, 0, st, p);
-  if (r.splits > 1) {
-    const int64_t n = (int64_t)p.a.B * p.a.c.heads * p.rows;
-    hipLaunchKernelGGL(k_attention_join<D>, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);
+  const dim3 g((unsigned)r.splits, (unsigned)r.tiles, (unsigned)(p.a.B * p.a.c.heads)), b(64 * r.waves);
+  if constexpr (D == 256) {
+    hipLaunchKernelGGL((k_attention<D, F, 1, 4, 1>), g, b, 0, st, p);
+  } else {
+    if (r.waves == 8) hipLaunchKernelGGL((k_attention<D, F, 1, 8, 2>), g, b, 0, st, p);
+    else if (r.nr == 1) hipLaunchKernelGGL((k_attention<D, F, 1, 4, 2>), g, b, 0, st, p);
+    else if (r.nr == 2) hipLaunchKernelGGL((k_attention<D, F, 2, 4, 2>), g, b, 0, st, p);
+    if constexpr (D == 64)
+      if (r.nr == 4) hipLaunchKernelGGL((k_attention<D, F, 4, 4, 2>), g, b, 0, st, p);
   }
+  if (r.splits > 1)
+    hipLaunchKernelGGL(k_attention_join<D>, dim3((unsigned)((int64_t)p.a.B * p.a.c.heads * p.rows)), dim3(256), 0, st,
+                       p);
   return hipGetLastError();
 }
 

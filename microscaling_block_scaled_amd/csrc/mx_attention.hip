@@ -511,14 +511,16 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
   }
 }
 
-// Joins the pieces of a row.  A workgroup takes a row, each of its waves every
-// fourth piece; their sums meet in LDS.
-template <int D>
+// Joins the pieces of a row.  W waves of a workgroup take a row, each of them every
+// W-th piece; their sums meet in LDS.
+template <int D, int W>
 __global__ __launch_bounds__(256) void k_attention_join(AttnArgs p) {
   __shared__ float part[4][D + 1];
+  const int64_t total = (int64_t)p.a.B * p.a.c.heads * p.rows;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t at = blockIdx.x;
+  const int64_t mine = (int64_t)blockIdx.x * (4 / W) + wave / W;
+  const int64_t at = mine < total ? mine : total - 1;  // past the last row: that one again, not stored
   const int row = (int)(at % p.rows);
   const int64_t bh = at / p.rows;
   const int head = (int)(bh % p.a.c.heads), b = (int)(bh / p.a.c.heads);
@@ -539,7 +541,7 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs p) {
   const float base = m == -__builtin_inff() ? 0.0f : m;
   float l = 0.0f, o[D / 64] = {};
 #pragma unroll 4
-  for (int s = wave; s < n; s += 4) {
+  for (int s = wave % W; s < n; s += W) {
     const float a = __builtin_amdgcn_exp2f(mls[2 * s] - base);
     l += mls[2 * s + 1] * a;
 #pragma unroll
@@ -549,13 +551,19 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs p) {
   for (int k = 0; k < D / 64; k++) part[wave][64 * k + lane] = o[k];
   if (lane == 0) part[wave][D] = l;
   __syncthreads();
-  l = part[0][D] + part[1][D] + part[2][D] + part[3][D];
+  if (mine >= total) return;
+  const int w0 = wave / W * W;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; w++) l += part[w0 + w][D];
   const int64_t tok = (int64_t)b * p.a.Lq + qt;
-  for (int d = threadIdx.x; d < D; d += 256) {
-    const float v = part[0][d] + part[1][d] + part[2][d] + part[3][d];
+  for (int d = (int)threadIdx.x % (64 * W); d < D; d += 64 * W) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; w++) v += part[w0 + w][d];
     p.a.o[tok * p.a.ld_o + (int64_t)hq * D + d] = __builtin_bit_cast(uint16_t, (__bf16)(l == 0.0f ? 0.0f : v / l));
   }
-  if (threadIdx.x == 0 && p.a.lse)
+  if (threadIdx.x % (64 * W) == 0 && p.a.lse)
     p.a.lse[tok * (p.a.c.heads * p.a.group) + hq] =
         l == 0.0f ? -__builtin_inff() : m * 0.69314718055994530942f + logf(l);
 }
@@ -603,9 +611,11 @@ hipError_t attention_by_rows(const AttnArgs& p, const Plan& r, hipStream_t st) {
     if constexpr (D == 64)
       if (r.nr == 4) hipLaunchKernelGGL((k_attention<D, F, 4, 4, 2>), g, b, 0, st, p);
   }
-  if (r.splits > 1)
-    hipLaunchKernelGGL(k_attention_join<D>, dim3((unsigned)((int64_t)p.a.B * p.a.c.heads * p.rows)), dim3(256), 0, st,
-                       p);
+  if (r.splits > 1) {  // 8192 rows: 12 us by four waves each, 6 by one; 32 rows of 64 pieces: 5 us and 20
+    const int64_t n = (int64_t)p.a.B * p.a.c.heads * p.rows;
+    if (n >= 2048) hipLaunchKernelGGL((k_attention_join<D, 1>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((k_attention_join<D, 4>), dim3((unsigned)n), dim3(256), 0, st, p);
+  }
   return hipGetLastError();
 }
 

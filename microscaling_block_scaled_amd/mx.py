@@ -215,11 +215,13 @@ def gemm_mx(a_q: torch.Tensor, a_s: torch.Tensor, a_fmt: int, b_q: torch.Tensor,
 _SRC = {torch.float32: SRC_F32, torch.bfloat16: SRC_BF16}
 
 
-def _on(stream, device):
-    """The HIP stream handle of a call, whose tensors must lie on the current device."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device, got {device}")
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _on(stream, t):
+    """The HIP stream handle of a call whose first tensor is t, which must lie on
+    the current device; and that device's number."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, dev
 
 
 def _empty(shape, dtype, device, stream):
@@ -238,31 +240,30 @@ def _new_rows(rows, cols, dtype, device, stream):
     return t if pitch == cols else t[:, :cols]
 
 
-def _rows(t, like, what):
-    """Checks a row-major matrix against another one; its address and pitch."""
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{what} must be {tuple(like.shape)} {like.dtype} on {like.device}")
-    st = t.stride()
-    if st[1] != 1 and t.shape[1] > 1:
+def _rows(t, shape, dtype, dev, what):
+    """Checks a row-major matrix; its address and pitch.  The pitch of a single row
+    says nothing: one that is allowed is given."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{what} must be a {tuple(shape)} {dtype} tensor on device {dev}")
+    pitch, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
         raise ValueError(f"{what} must have unit column stride")
-    return t.data_ptr(), _pitch(t, st)
+    return t.data_ptr(), pitch if shape[0] > 1 else -(-shape[1] // 8) * 8
 
 
-def _pitch(t, st):
-    # the pitch of a single row says nothing: any that is allowed will do
-    return st[0] if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
-
-
-def _vector(t, n, dtype, device, what):
-    if t.shape != (n,) or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} on {device}")
+def _flat(t, shape, dtype, dev, what):
+    """Checks a contiguous tensor; its address."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on device {dev}")
     return t.data_ptr()
 
 
-def _out(t, shape, dtype, device, what):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {shape} {dtype} tensor on {device}")
-    return t.data_ptr()
+def _work(t, dev):
+    if t is None:
+        return None, 0
+    if t.dtype != torch.uint8 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on device {dev}")
+    return t.data_ptr(), t.numel()
 
 
 def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, fmt: int, eps: float = 1e-5,
@@ -273,31 +274,33 @@ def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, fmt: int, eps: float = 1e
     [rows] fp32, h where a residual is given, and y in x's type where ``want_y``
     is set; ``out`` may supply any of them preallocated (h may be x or the
     residual)."""
-    if x.dim() != 2 or x.dtype not in _SRC:
-        raise ValueError("x must be a 2-D fp32/bf16 CUDA tensor")
-    handle, dev = _on(stream, x.device), x.device
-    rows, cols = x.shape
-    px, ld_x = _rows(x, x, "x")
-    pr, ld_r = (None, 0) if residual is None else _rows(residual, x, "residual")
-    pw = _vector(w, cols, x.dtype, dev, "w")
-    o = dict(out or {})
-    packed, nblk = packed_bytes(fmt, 1, cols), (cols + 31) // 32
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if len(shape) != 2 or dtype not in _SRC or fmt not in BITS:
+        raise ValueError("x must be a 2-D fp32/bf16 CUDA tensor, fmt a format")
+    handle, dev = _on(stream, x)
+    rows, cols = shape
+    px, ld_x = _rows(x, shape, dtype, dev, "x")
+    pr, ld_r = (None, 0) if residual is None else _rows(residual, shape, dtype, dev, "residual")
+    pw = _flat(w, (cols,), dtype, dev, "w")
+    o = dict(out) if out else {}
+    nblk = (cols + 31) // 32
+    packed = nblk * 4 * BITS[fmt]
     if "q_row" not in o:
-        o["q_row"] = _empty((rows, packed), torch.uint8, dev, stream)
+        o["q_row"] = _empty((rows, packed), torch.uint8, device, stream)
     if "s_row" not in o:
-        o["s_row"] = _empty((rows, nblk), torch.uint8, dev, stream)
+        o["s_row"] = _empty((rows, nblk), torch.uint8, device, stream)
     if "rstd" not in o:
-        o["rstd"] = _empty((rows,), torch.float32, dev, stream)
+        o["rstd"] = _empty((rows,), torch.float32, device, stream)
     if residual is not None and "h" not in o:
-        o["h"] = _new_rows(rows, cols, x.dtype, dev, stream)
+        o["h"] = _new_rows(rows, cols, dtype, device, stream)
     if want_y and "y" not in o:
-        o["y"] = _new_rows(rows, cols, x.dtype, dev, stream)
-    ph, ld_h = _rows(o["h"], x, "h") if "h" in o else (None, 0)
-    py, ld_y = _rows(o["y"], x, "y") if "y" in o else (None, 0)
-    _check(lib.mx_rmsnorm_quantize(px, ld_x, pr, ld_r, pw, rows, cols, _SRC[x.dtype], fmt, eps, ph, ld_h, py, ld_y,
-                                   _out(o["q_row"], (rows, packed), torch.uint8, dev, "q_row"),
-                                   _out(o["s_row"], (rows, nblk), torch.uint8, dev, "s_row"),
-                                   _vector(o["rstd"], rows, torch.float32, dev, "rstd"), handle),
+        o["y"] = _new_rows(rows, cols, dtype, device, stream)
+    ph, ld_h = _rows(o["h"], shape, dtype, dev, "h") if "h" in o else (None, 0)
+    py, ld_y = _rows(o["y"], shape, dtype, dev, "y") if "y" in o else (None, 0)
+    _check(lib.mx_rmsnorm_quantize(px, ld_x, pr, ld_r, pw, rows, cols, _SRC[dtype], fmt, eps, ph, ld_h, py, ld_y,
+                                   _flat(o["q_row"], (rows, packed), torch.uint8, dev, "q_row"),
+                                   _flat(o["s_row"], (rows, nblk), torch.uint8, dev, "s_row"),
+                                   _flat(o["rstd"], (rows,), torch.float32, dev, "rstd"), handle),
            "mx_rmsnorm_quantize")
     return o
 
@@ -309,51 +312,48 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: t
     (and so of x and the residual), in h's type, with dh, what reaches h another
     way, added; and dw in fp32.  ``out`` and ``workspace`` (a uint8 tensor) may
     be supplied."""
-    if h.dim() != 2 or h.dtype not in _SRC:
+    shape, dtype, device = h.shape, h.dtype, h.device
+    if len(shape) != 2 or dtype not in _SRC:
         raise ValueError("h must be a 2-D fp32/bf16 CUDA tensor")
-    handle, dev = _on(stream, h.device), h.device
-    rows, cols = h.shape
-    src = _SRC[h.dtype]
-    pdy, ld_dy = _rows(dy, h, "dy")
-    ph, ld_h = _rows(h, h, "h")
-    pdh, ld_dh = (None, 0) if dh is None else _rows(dh, h, "dh")
-    o = dict(out or {})
+    handle, dev = _on(stream, h)
+    rows, cols = shape
+    src = _SRC[dtype]
+    pdy, ld_dy = _rows(dy, shape, dtype, dev, "dy")
+    ph, ld_h = _rows(h, shape, dtype, dev, "h")
+    pdh, ld_dh = (None, 0) if dh is None else _rows(dh, shape, dtype, dev, "dh")
+    o = dict(out) if out else {}
     if "dx" not in o:
-        o["dx"] = _new_rows(rows, cols, h.dtype, dev, stream)
+        o["dx"] = _new_rows(rows, cols, dtype, device, stream)
     if "dw" not in o:
-        o["dw"] = _empty((cols,), torch.float32, dev, stream)
+        o["dw"] = _empty((cols,), torch.float32, device, stream)
     if workspace is None:
-        workspace = _empty((max(0, lib.mx_rmsnorm_backward_workspace(rows, cols, src)),), torch.uint8, dev, stream)
-    pdx, ld_dx = _rows(o["dx"], h, "dx")
-    _check(lib.mx_rmsnorm_backward(pdy, ld_dy, ph, ld_h, _vector(w, cols, h.dtype, dev, "w"),
-                                   _vector(rstd, rows, torch.float32, dev, "rstd"), pdh, ld_dh, rows, cols, src,
-                                   pdx, ld_dx, _vector(o["dw"], cols, torch.float32, dev, "dw"),
+        workspace = _empty((max(0, lib.mx_rmsnorm_backward_workspace(rows, cols, src)),), torch.uint8, device,
+                           stream)
+    pdx, ld_dx = _rows(o["dx"], shape, dtype, dev, "dx")
+    _check(lib.mx_rmsnorm_backward(pdy, ld_dy, ph, ld_h, _flat(w, (cols,), dtype, dev, "w"),
+                                   _flat(rstd, (rows,), torch.float32, dev, "rstd"), pdh, ld_dh, rows, cols, src,
+                                   pdx, ld_dx, _flat(o["dw"], (cols,), torch.float32, dev, "dw"),
                                    *_work(workspace, dev), handle), "mx_rmsnorm_backward")
     return o
 
 
-def _work(t, device):
-    if t is None:
-        return None, 0
-    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return t.data_ptr(), t.numel()
-
-
 def _gemv(call, dtype, what, x, w_q, w_s, w_fmt, M, N, K, y, stream):
-    handle, dev = _on(stream, x.device), x.device
-    if x.shape != (M, K) or x.dtype != torch.bfloat16:
-        raise ValueError("x must be a bf16 [M, K] tensor")
-    if x.stride(1) != 1 and K > 1:
-        raise ValueError("x must have unit column stride")
-    pw = _out(w_q, (N, packed_bytes(w_fmt, 1, K)), torch.uint8, dev, "w_q")
-    ps = _out(w_s, (N, (K + 31) // 32), torch.uint8, dev, "w_s")
+    handle, dev = _on(stream, x)
+    if w_fmt not in BITS:
+        raise ValueError("w_fmt must be a format")
+    if x.shape != (M, K) or x.dtype != torch.bfloat16 or (K > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a bf16 [M, K] tensor with unit column stride")
+    nblk = (K + 31) // 32
+    pw = _flat(w_q, (N, nblk * 4 * BITS[w_fmt]), torch.uint8, dev, "w_q")
+    ps = _flat(w_s, (N, nblk), torch.uint8, dev, "w_s")
     if y is None:
-        y = _empty((M, N), dtype, dev, stream)
-    if y.shape != (M, N) or y.dtype != dtype or y.device != dev or (y.stride(1) != 1 and N > 1):
-        raise ValueError(f"y must be a {dtype} [M, N] tensor with unit column stride")
-    _check(call(x.data_ptr(), x.stride(0) if M > 1 else K, pw, ps, w_fmt, M, N, K, y.data_ptr(),
-                y.stride(0) if M > 1 else N, handle), what)
+        y = _empty((M, N), dtype, x.device, stream)
+        ld_y = N
+    else:
+        if y.shape != (M, N) or y.dtype != dtype or y.get_device() != dev or (N > 1 and y.stride(1) != 1):
+            raise ValueError(f"y must be a {dtype} [M, N] tensor with unit column stride")
+        ld_y = y.stride(0) if M > 1 else N
+    _check(call(x.data_ptr(), x.stride(0) if M > 1 else K, pw, ps, w_fmt, M, N, K, y.data_ptr(), ld_y, handle), what)
     return y
 
 
@@ -377,14 +377,15 @@ def kv_cache(pages: int, heads: int, page: int, dim: int, device="cuda") -> dict
     return {"k_q": e(dim), "k_s": e(dim // 32), "v_q": e(dim), "v_s": e(dim // 32)}
 
 
-def _cache(c, fmt, device):
-    kq = c["k_q"]
+def _cache(c, fmt, dev):
+    kq, u8 = c["k_q"], torch.uint8
     if kq.dim() != 4:
         raise ValueError("k_q must be [pages, heads, page, dim]")
-    pages, heads, page, dim = shape = kq.shape
+    shape = kq.shape
+    pages, heads, page, dim = shape
     scales = (pages, heads, page, dim // 32)
-    return Cache(_out(kq, shape, torch.uint8, device, "k_q"), _out(c["k_s"], scales, torch.uint8, device, "k_s"),
-                 _out(c["v_q"], shape, torch.uint8, device, "v_q"), _out(c["v_s"], scales, torch.uint8, device, "v_s"),
+    return Cache(_flat(kq, shape, u8, dev, "k_q"), _flat(c["k_s"], scales, u8, dev, "k_s"),
+                 _flat(c["v_q"], shape, u8, dev, "v_q"), _flat(c["v_s"], scales, u8, dev, "v_s"),
                  pages, heads, page, dim, fmt)
 
 
@@ -392,21 +393,23 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: di
     """Quantizes the keys and values of some tokens (fp32 or bf16 [tokens, heads,
     dim]) into a cache (``kv_cache``): token t goes to place slots[t] % page of
     page slots[t] // page; a slot outside the cache (-1) is not written."""
-    handle, dev = _on(stream, k.device), k.device
+    handle, dev = _on(stream, k)
     c = _cache(cache, fmt, dev)
-    if k.dim() != 3 or k.dtype not in _SRC or v.dtype != k.dtype or v.shape != k.shape or v.device != dev:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or dtype not in _SRC or v.dtype != dtype or v.shape != shape or v.get_device() != dev:
         raise ValueError("k and v must be fp32/bf16 [tokens, heads, dim] tensors of one type")
-    tokens = k.shape[0]
-    if k.shape[1:] != (c.heads, c.dim):
+    tokens = shape[0]
+    if shape[1:] != (c.heads, c.dim):
         raise ValueError(f"k must be [tokens, {c.heads}, {c.dim}]")
-    sk, sv = k.stride(), v.stride()
-    if sk[2] != 1 or sv[2] != 1:
+    (ld_k, hs_k, unit_k), (ld_v, hs_v, unit_v) = k.stride(), v.stride()
+    if unit_k != 1 or unit_v != 1:
         raise ValueError("k and v must have unit stride along dim")
-    one = tokens <= 1  # the stride of a single token or head says nothing
-    hs_k, hs_v = (c.dim, c.dim) if c.heads <= 1 else (sk[1], sv[1])
-    _check(lib.mx_cache_write(ctypes.byref(c), k.data_ptr(), 0 if one else sk[0], hs_k, v.data_ptr(),
-                              0 if one else sv[0], hs_v, _SRC[k.dtype], tokens,
-                              _vector(slots, tokens, torch.int64, dev, "slots"), handle), "mx_cache_write")
+    if tokens <= 1:  # the stride of a single token or head says nothing
+        ld_k = ld_v = 0
+    if c.heads <= 1:
+        hs_k = hs_v = c.dim
+    _check(lib.mx_cache_write(c, k.data_ptr(), ld_k, hs_k, v.data_ptr(), ld_v, hs_v, _SRC[dtype], tokens,
+                              _flat(slots, (tokens,), torch.int64, dev, "slots"), handle), "mx_cache_write")
 
 
 def attention(q: torch.Tensor, cache: dict, fmt: int, table: torch.Tensor, lens: torch.Tensor,
@@ -418,34 +421,35 @@ def attention(q: torch.Tensor, cache: dict, fmt: int, table: torch.Tensor, lens:
     lens - Lq + i + 1.  Returns o like q and lse [B, Lq, query heads] fp32.
     ``max_len``: a bound of lens (default: what the table holds); ``scale``:
     default 1 / sqrt(dim); ``out`` and ``workspace`` may be supplied."""
-    handle, dev = _on(stream, q.device), q.device
+    handle, dev = _on(stream, q)
     c = _cache(cache, fmt, dev)
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or q.shape[3] != c.dim:
-        raise ValueError(f"q must be a bf16 [B, Lq, query heads, {c.dim}] tensor")
-    B, Lq, heads_q, dim = q.shape
+    shape, dim = q.shape, c.dim
+    if len(shape) != 4 or q.dtype != torch.bfloat16 or shape[3] != dim:
+        raise ValueError(f"q must be a bf16 [B, Lq, query heads, {dim}] tensor")
+    B, Lq, heads_q, _ = shape
     sq = q.stride()
     if sq[3] != 1 or (sq[2] != dim and heads_q > 1) or (sq[0] != Lq * sq[1] and B > 1 and Lq > 1):
         raise ValueError("q must have contiguous heads and evenly spaced tokens")
     ld_q = sq[1] if Lq > 1 else sq[0] if B > 1 else heads_q * dim
-    if table.dim() != 2 or table.shape[0] != B or table.dtype != torch.int32 or table.device != dev or \
-            (table.stride(1) != 1 and table.shape[1] > 1):
+    if table.dim() != 2 or table.dtype != torch.int32 or table.get_device() != dev or table.shape[0] != B or \
+            (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be an int32 [B, pages] tensor with unit column stride")
     per = table.shape[1]
     if max_len is None:
         max_len = per * c.page
-    o = dict(out or {})
+    o = dict(out) if out else {}
     if "o" not in o:
-        o["o"] = _empty((B, Lq, heads_q, dim), torch.bfloat16, dev, stream)
+        o["o"] = _empty(shape, torch.bfloat16, q.device, stream)
     if "lse" not in o:
-        o["lse"] = _empty((B, Lq, heads_q), torch.float32, dev, stream)
+        o["lse"] = _empty(shape[:3], torch.float32, q.device, stream)
     if workspace is None:
         need = lib.mx_attention_workspace(B, Lq, heads_q, c.heads, dim, max_len)
         if need > 0:
-            workspace = _empty((need,), torch.uint8, dev, stream)
-    _check(lib.mx_attention(ctypes.byref(c), q.data_ptr(), ld_q, table.data_ptr(),
-                            table.stride(0) if B > 1 else per, _vector(lens, B, torch.int32, dev, "lens"), B, Lq,
-                            heads_q, dim ** -0.5 if scale is None else scale, max_len,
-                            _out(o["o"], (B, Lq, heads_q, dim), torch.bfloat16, dev, "o"), heads_q * dim,
-                            _out(o["lse"], (B, Lq, heads_q), torch.float32, dev, "lse"),
-                            *_work(workspace, dev), handle), "mx_attention")
+            workspace = _empty((need,), torch.uint8, q.device, stream)
+    _check(lib.mx_attention(c, q.data_ptr(), ld_q, table.data_ptr(), table.stride(0) if B > 1 else per,
+                            _flat(lens, (B,), torch.int32, dev, "lens"), B, Lq, heads_q,
+                            dim ** -0.5 if scale is None else scale, max_len,
+                            _flat(o["o"], shape, torch.bfloat16, dev, "o"), heads_q * dim,
+                            _flat(o["lse"], shape[:3], torch.float32, dev, "lse"), *_work(workspace, dev), handle),
+           "mx_attention")
     return o

@@ -26,34 +26,41 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // ---------------------------------------------------------------------------
 // cache write
 // ---------------------------------------------------------------------------
-// A lane takes 8 elements of a token's head, a quad one block.  Bound: HBM.
+// A lane takes 8 elements of a token's head, keys and values (two loads in flight), a
+// quad one block.  Bound: HBM; at few tokens the launch.  Tokens of few elements
+// share a workgroup.
 template <int SRC, int F>
-__global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p) {
-  constexpr int ESZ = SRC == SRC_BF16 ? 2 : 4;
-  const int chunks = p.c.dim / 8, per = 2 * p.c.heads * chunks;  // of a token: keys, then values
-  const int64_t n = p.tokens * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t tok = i / per;
-    int rest = (int)(i - tok * per);
-    const bool value = rest >= per / 2;
-    if (value) rest -= per / 2;
-    const int head = rest / chunks, c = rest - head * chunks;
-    const int64_t slot = p.slots[tok];  // the same for the lanes of a quad
-    if (slot < 0 || slot >= p.c.pages * p.c.page) continue;
-    const uint8_t* src = value ? (const uint8_t*)p.v + tok * p.ld_v + head * p.hs_v
-                               : (const uint8_t*)p.k + tok * p.ld_k + head * p.hs_k;
-    uint32_t raw[2 * ESZ], v[8], am = 0, rnd[8];
-    load_elems<ESZ, 8, false>(src + (int64_t)c * 8 * ESZ, 8, raw);
-    widen8<SRC>(raw, v);
+__device__ __forceinline__ void write_chunk(const uint32_t* raw, uint8_t* q, uint8_t* s, int c) {
+  uint32_t v[8], am = 0, rnd[8];
+  widen8<SRC>(raw, v);
 #pragma unroll
-    for (int k = 0; k < 8; k++) am = umax(am, v[k] & 0x7FFFFFFFu);
-    am = umax(am, quad_xor1(am));
-    am = umax(am, quad_xor2(am));
-    const uint32_t code = scale_code<F>(am);
-    const int64_t pg = slot / p.c.page;
-    const int64_t row = (pg * p.c.heads + head) * p.c.page + (slot - pg * p.c.page);
-    if ((c & 3) == 0) (value ? p.c.v_s : p.c.k_s)[row * (p.c.dim / 32) + (c >> 2)] = (uint8_t)code;
-    store8<F, false>((value ? p.c.v_q : p.c.k_q) + row * p.c.dim, c, convert8<F, false>(v, code, rnd));
+  for (int k = 0; k < 8; k++) am = umax(am, v[k] & 0x7FFFFFFFu);
+  am = umax(am, quad_xor1(am));
+  am = umax(am, quad_xor2(am));
+  const uint32_t code = scale_code<F>(am);
+  if ((c & 3) == 0) s[c >> 2] = (uint8_t)code;
+  store8<F, false>(q, c, convert8<F, false>(v, code, rnd));
+}
+
+template <int SRC, int F>
+__global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift, int tokens_per_wg) {
+  constexpr int ESZ = SRC == SRC_BF16 ? 2 : 4;
+  const int per = p.c.heads << shift;  // chunks of a token's keys; 1 << shift of a head's
+  const int sub = tokens_per_wg > 1 ? (int)threadIdx.x / per : 0;
+  const int64_t tok = (int64_t)blockIdx.x * tokens_per_wg + sub;
+  if (sub >= tokens_per_wg || tok >= p.tokens) return;
+  const int64_t slot = p.slots[tok];  // the same for the lanes of a quad
+  if (slot < 0 || slot >= p.c.pages * p.c.page) return;
+  const int64_t pg = slot / p.c.page;
+  const int at = (int)(slot - pg * p.c.page);
+  for (int i = (int)threadIdx.x - sub * per; i < per; i += 256) {
+    const int head = i >> shift, c = i & ((1 << shift) - 1);
+    uint32_t k[2 * ESZ], v[2 * ESZ];
+    load_elems<ESZ, 8, false>((const uint8_t*)p.k + tok * p.ld_k + head * p.hs_k + c * 8 * ESZ, 8, k);
+    load_elems<ESZ, 8, false>((const uint8_t*)p.v + tok * p.ld_v + head * p.hs_v + c * 8 * ESZ, 8, v);
+    const int64_t row = (pg * p.c.heads + head) * p.c.page + at;
+    write_chunk<SRC, F>(k, p.c.k_q + row * p.c.dim, p.c.k_s + row * (p.c.dim / 32), c);
+    write_chunk<SRC, F>(v, p.c.v_q + row * p.c.dim, p.c.v_s + row * (p.c.dim / 32), c);
   }
 }
 
@@ -627,16 +634,15 @@ hipError_t attention_by_fmt(const AttnArgs& p, const Plan& r, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_cache_write(const CacheWriteArgs& a, hipStream_t st) {
-  const int64_t n = a.tokens * (2 * a.c.heads * (a.c.dim / 8));
-  int64_t blocks = (n + 255) / 256;
-  if (blocks > 65536) blocks = 65536;
-  const dim3 g((unsigned)blocks), b(256);
+  const int shift = a.c.dim == 64 ? 3 : a.c.dim == 128 ? 4 : 5, per = a.c.heads << shift;
+  const int tpw = per >= 256 ? 1 : 256 / per;
+  const dim3 g((unsigned)((a.tokens + tpw - 1) / tpw)), b(256);
   if (a.src == SRC_BF16) {
-    if (a.c.fmt == E4M3) hipLaunchKernelGGL((k_cache_write<SRC_BF16, E4M3>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_cache_write<SRC_BF16, E5M2>), g, b, 0, st, a);
+    if (a.c.fmt == E4M3) hipLaunchKernelGGL((k_cache_write<SRC_BF16, E4M3>), g, b, 0, st, a, shift, tpw);
+    else hipLaunchKernelGGL((k_cache_write<SRC_BF16, E5M2>), g, b, 0, st, a, shift, tpw);
   } else {
-    if (a.c.fmt == E4M3) hipLaunchKernelGGL((k_cache_write<SRC_F32, E4M3>), g, b, 0, st, a);
-    else hipLaunchKernelGGL((k_cache_write<SRC_F32, E5M2>), g, b, 0, st, a);
+    if (a.c.fmt == E4M3) hipLaunchKernelGGL((k_cache_write<SRC_F32, E4M3>), g, b, 0, st, a, shift, tpw);
+    else hipLaunchKernelGGL((k_cache_write<SRC_F32, E5M2>), g, b, 0, st, a, shift, tpw);
   }
   return hipGetLastError();
 }

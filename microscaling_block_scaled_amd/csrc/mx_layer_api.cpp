@@ -189,6 +189,7 @@ int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t h
   if (!src_ok(src) || tokens < 0 || ld_k < 0 || hs_k < 0 || ld_v < 0 || hs_v < 0) return MX_ERR_ARG;
   if (tokens == 0 || cache->heads == 0 || cache->pages == 0) return MX_OK;
   if (!k || !v || !slots) return MX_ERR_ARG;
+  if (tokens >= kMaxRows) return MX_ERR_UNSUPPORTED;
   const int64_t esz = esz_of(src);
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || (ld_k * esz) % 16 || (hs_k * esz) % 16 ||
       (ld_v * esz) % 16 || (hs_v * esz) % 16)

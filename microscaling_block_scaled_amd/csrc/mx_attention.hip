@@ -77,8 +77,9 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift
 //   O^T = V^T P^T those 8 scores (two groups of 16 tokens) are the lane's 8 of the
 //                 32 of a sum over tokens as they are; the lane takes dims
 //                 (l % 16) D/16 .. of the same 8 tokens and transposes 2 x 2
-// so P stays in registers.  P is rounded to bf16 (relative error 2^-9, of the size of
-// the output's own rounding); scores, maxima, sums and O stay in fp32.
+// so P stays in registers.  P is rounded to bf16 (up to 2^-8 of itself, like the
+// output's own rounding; its sum l is of the unrounded p); scores, maxima, sums and O
+// stay in fp32.
 //
 // Bound for a few rows: HBM, 2 (D + D / 32) bytes a token and head.  Each wave loads
 // its 32 tokens in whole 1 KB runs and reads them again from its own piece of LDS:
@@ -315,7 +316,11 @@ __device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[D / 32
       }
     }
   }
-  if (cut) {
+#pragma unroll
+  for (int n = 0; n < NR; n++)
+#pragma unroll
+    for (int u = 0; u < 2; u++) s[n][u] *= scale2;
+  if (cut) {  // after the scaling, whose sign is the caller's
 #pragma unroll
     for (int n = 0; n < NR; n++)
 #pragma unroll
@@ -331,7 +336,7 @@ __device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[D / 32
     float v[8], top = -__builtin_inff();
 #pragma unroll
     for (int e = 0; e < 8; e++) {
-      v[e] = s[n][e >> 2][e & 3] * scale2;
+      v[e] = s[n][e >> 2][e & 3];
       top = __builtin_fmaxf(top, v[e]);
     }
     const float m = __builtin_fmaxf(sum.m[n], rows_max(top));

@@ -234,6 +234,7 @@ int mx_attention(const mx_cache* cache, const void* q, int64_t ld_q, const int32
     if (!aligned(workspace, 16)) return MX_ERR_ALIGN;
     if (workspace_bytes < need) return MX_ERR_SHAPE;
   }
+  if (cache->pages == 0) max_len = 0;  // there are no tokens, and no memory that stands in for absent ones
   mx::AttentionArgs a;
   a.c = cache_of(cache);
   a.q = (const uint16_t*)q;

@@ -67,8 +67,8 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
-// Rows of a key/value head are its (query token, query head) pairs; a workgroup
-// takes NR tiles of 16 of them and one piece of the request's tokens, each wave 32
+// Rows of a key/value head are its (query token, query head) pairs.  Up to 16 of them:
+// a workgroup takes them all and one piece of the request's tokens, each wave 32
 // tokens at a time.  Both products run on 16x16x32 bf16 matrix instructions, to
 // which an element times its scale is exact:
 //   S^T = K Q^T   lane (l % 16, g = l / 16) takes dims g D/4 .. of token l % 16 and
@@ -96,8 +96,9 @@ struct AttnArgs {
   int splits;
   int chunk;             // tokens of a piece, a multiple of what its waves take at a time
   uint32_t page16, magic;  // page / 16 and the constant that divides by it
-  float* part_o;         // [B][heads][rows][splits][dim]
-  float* part_ml;        // [B][heads][rows][splits][2]
+  // sums and (base, l) of the pieces: by rows [B][heads][rows][splits][dim] and [2], or
+  // by tiles of 16 rows [B][heads][tiles][splits][dim / 16][64 lanes][4] and [16][2]
+  float *part_o, *part_ml;
 };
 
 template <int F>
@@ -149,27 +150,36 @@ struct Stage {
   static constexpr int BYTES = VS_AT + 32 * SP;
 };
 
-// Where tokens 16 u .. of a request lie: row (page, head, place) of the cache.
-// A page that is not one of the cache's holds no tokens.
-__device__ __forceinline__ bool locate(const AttnArgs& p, const int32_t* table, int head, int tok, int64_t& row) {
+// The page of tokens t0 + 16 (l & 1) .. of a request in lane l, -1 where there are
+// none.  By a vector load and a step ahead of its use: a wave that waits for a page
+// number before it can load tokens does nothing else meanwhile.
+__device__ __forceinline__ int page_of(const AttnArgs& p, const int32_t* table, int t0, int end) {
+  const int tok = t0 + 16 * (int)(threadIdx.x & 1);
+  if (tok >= end) return -1;
   const uint32_t i16 = (uint32_t)tok >> 4;
+  return table[p.page16 == 1 ? i16 : __umulhi(i16, p.magic)];
+}
+// Row (page, head, place) of the cache at which tokens t0 + 16 u .. begin.  A page
+// that is not one of the cache's holds no tokens; any row stands in for it, and what
+// it holds is masked.
+__device__ __forceinline__ bool locate(const AttnArgs& p, int pages, int head, int t0, int u, int64_t& row) {
+  const int pg = __builtin_amdgcn_readlane(pages, u);
+  const uint32_t i16 = (uint32_t)(t0 + 16 * u) >> 4;
   const uint32_t idx = p.page16 == 1 ? i16 : __umulhi(i16, p.magic);
-  const int pg = table[idx];
-  row = ((int64_t)pg * p.a.c.heads + head) * p.a.c.page + (int)(i16 - idx * p.page16) * 16;
-  return (uint32_t)pg < (uint32_t)p.a.c.pages;
+  const bool ok = (uint32_t)pg < (uint32_t)p.a.c.pages;
+  row = ok ? ((int64_t)pg * p.a.c.heads + head) * p.a.c.page + (int)(i16 - idx * p.page16) * 16 : 0;
+  return ok;
 }
 
 template <int D>
-__device__ __forceinline__ uint32_t load_step(const AttnArgs& p, const int32_t* table, int head, int t0, int end,
+__device__ __forceinline__ uint32_t load_step(const AttnArgs& p, int pages, int head, int t0,
                                               Raw<D>& x) {
   const uint32_t lane = threadIdx.x & 63;
   uint32_t there = 0;
   int64_t row[2];
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    bool ok = t0 + 16 * u < end;
-    if (ok) ok = locate(p, table, head, t0 + 16 * u, row[u]);
-    if (!ok) row[u] = 0;  // any row of the cache: what it holds is masked
+    const bool ok = locate(p, pages, head, t0, u, row[u]);
     there |= (uint32_t)ok << u;
   }
 #pragma unroll
@@ -279,18 +289,50 @@ struct Sums {
   float m[NR], l[NR];   // l over the lane's tokens only
 };
 
+// Maxima, weights and sums of a step's scores (in units of log 2, masked); p as the
+// operand of the second product.  The base that scores are taken from is a maximum of
+// earlier ones: it moves, and the sums with it, only where a score passes it by more
+// than 8, so p stays below 2^8 and O is seldom multiplied.  o / l does not depend on
+// the base.
+template <int D, int NR>
+__device__ __forceinline__ void soften(f32x4 (&s)[NR][2], Sums<D, NR>& sum, bf16x8 (&pr)[NR]) {
+#pragma unroll
+  for (int n = 0; n < NR; n++) {
+    float v[8], top = -__builtin_inff();
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      v[e] = s[n][e >> 2][e & 3];
+      top = __builtin_fmaxf(top, v[e]);
+    }
+    top = rows_max(top);
+    if (__any(top > sum.m[n] + 8.0f)) {
+      const float m = __builtin_fmaxf(sum.m[n], top);
+      const float a = __builtin_amdgcn_exp2f(sum.m[n] - (m == -__builtin_inff() ? 0.0f : m));
+      sum.m[n] = m;
+      sum.l[n] *= a;
+#pragma unroll
+      for (int d = 0; d < D / 16; d++) sum.o[n][d] *= a;
+    }
+    const float base = sum.m[n] == -__builtin_inff() ? 0.0f : sum.m[n];  // nothing seen yet: every p is 0
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      v[e] = __builtin_amdgcn_exp2f(v[e] - base);
+      sum.l[n] += v[e];
+    }
+    pr[n] = operand(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+  }
+}
+
 // One step of 32 staged tokens.  `cut`: some row does not see all of them, or some
-// are not there.  limit[n] is the number of them that the lane's row sees (less than
-// 1: none, 32 or more: all).  `odd`: values may not be finite and rows see different
+// are not there.  `limit` is the number of them that the lane's row sees (less than 1:
+// none, 32 or more: all).  `odd`: values may not be finite and rows see different
 // tokens.
-template <int D, int F, int NR>
-__device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[D / 32][64], float scale2, bool cut,
-                                          bool odd, uint32_t there, const int (&limit)[NR], Sums<D, NR>& sum) {
+template <int D, int F>
+__device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[64], float scale2, bool cut,
+                                          bool odd, uint32_t there, int limit, Sums<D, 1>& sum) {
   using St = Stage<D>;
   const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-  f32x4 s[NR][2];
-#pragma unroll
-  for (int n = 0; n < NR; n++) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
+  f32x4 s[1][2] = {{f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
 #pragma unroll
   for (int c = 0; c < D / 64; c++) {  // 16 bytes: dims g D/4 + 16 c .. of token 16 u + i
     uint4 kw[2];
@@ -308,82 +350,49 @@ __device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[D / 32
         const uint32_t w0 = h ? kw[u].z : kw[u].x, w1 = h ? kw[u].w : kw[u].y;
         k[u] = operand(cvt_lo<F>(w0, ks[u]), cvt_hi<F>(w0, ks[u]), cvt_lo<F>(w1, ks[u]), cvt_hi<F>(w1, ks[u]));
       }
+      const bf16x8 qj = q[2 * c + h][threadIdx.x & 63];
 #pragma unroll
-      for (int n = 0; n < NR; n++) {
-        const bf16x8 qj = q[n][2 * c + h][threadIdx.x & 63];
-#pragma unroll
-        for (int u = 0; u < 2; u++) s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u], qj, s[n][u], 0, 0, 0);
-      }
+      for (int u = 0; u < 2; u++) s[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u], qj, s[0][u], 0, 0, 0);
     }
   }
 #pragma unroll
-  for (int n = 0; n < NR; n++)
-#pragma unroll
-    for (int u = 0; u < 2; u++) s[n][u] *= scale2;
+  for (int u = 0; u < 2; u++) s[0][u] *= scale2;
   if (cut) {  // after the scaling, whose sign is the caller's
 #pragma unroll
-    for (int n = 0; n < NR; n++)
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const int tok = 16 * (e >> 2) + 4 * g + (e & 3);
-        const bool seen = tok < limit[n] && (there >> (e >> 2) & 1);
-        s[n][e >> 2][e & 3] = seen ? s[n][e >> 2][e & 3] : -__builtin_inff();
-      }
-  }
-  bf16x8 pr[NR];
-#pragma unroll
-  for (int n = 0; n < NR; n++) {
-    float v[8], top = -__builtin_inff();
-#pragma unroll
     for (int e = 0; e < 8; e++) {
-      v[e] = s[n][e >> 2][e & 3];
-      top = __builtin_fmaxf(top, v[e]);
+      const int tok = 16 * (e >> 2) + 4 * g + (e & 3);
+      const bool seen = tok < limit && (there >> (e >> 2) & 1);
+      s[0][e >> 2][e & 3] = seen ? s[0][e >> 2][e & 3] : -__builtin_inff();
     }
-    const float m = __builtin_fmaxf(sum.m[n], rows_max(top));
-    const float base = m == -__builtin_inff() ? 0.0f : m;  // nothing seen yet: every p is 0
-    if (__any(m != sum.m[n])) {
-      const float a = __builtin_amdgcn_exp2f(sum.m[n] - base);
-      sum.m[n] = m;
-      sum.l[n] *= a;
-#pragma unroll
-      for (int d = 0; d < D / 16; d++) sum.o[n][d] *= a;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      v[e] = __builtin_amdgcn_exp2f(v[e] - base);
-      sum.l[n] += v[e];
-    }
-    pr[n] = operand(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
   }
+  bf16x8 pr[1];
+  soften<D, 1>(s, sum, pr);
   if (odd) {
     // 0 * NaN is not 0: token by token, for the rows that see it.  p takes the
     // place of the keys.
+    wave_fence();
+    uint16_t* ps = (uint16_t*)(lds + St::K_AT);  // [row][token]
+    *(uint2*)(ps + 32 * i + 4 * g) = __builtin_bit_cast(u64x2, pr[0]).lo;
+    *(uint2*)(ps + 32 * i + 16 + 4 * g) = __builtin_bit_cast(u64x2, pr[0]).hi;
+    wave_fence();
+    for (int tok = 0; tok < STEP; tok++) {
+      if (tok >= limit) continue;
+      const float pt = __builtin_bit_cast(float, (uint32_t)ps[32 * i + tok] << 16);
 #pragma unroll
-    for (int n = 0; n < NR; n++) {
-      wave_fence();
-      uint16_t* ps = (uint16_t*)(lds + St::K_AT);  // [row][token]
-      *(uint2*)(ps + 32 * i + 4 * g) = __builtin_bit_cast(u64x2, pr[n]).lo;
-      *(uint2*)(ps + 32 * i + 16 + 4 * g) = __builtin_bit_cast(u64x2, pr[n]).hi;
-      wave_fence();
-      for (int tok = 0; tok < STEP; tok++) {
-        if (tok >= limit[n]) continue;
-        const float pt = __builtin_bit_cast(float, (uint32_t)ps[32 * i + tok] << 16);
+      for (int e = 0; e < 4; e++)
 #pragma unroll
-        for (int e = 0; e < 4; e++)
+        for (int k = 0; k < D / 64; k++) {
+          const int at = (4 * g + e) * (D / 16) + 4 * k;  // dims at .. at + 3
+          const uint32_t raw = *(const uint32_t*)(lds + St::V_AT + tok * St::VP + at);
+          const float sc = e8m0(lds[St::VS_AT + tok * St::SP + at / 32]);
+          const uint32_t a = cvt_lo<F>(raw, sc), b = cvt_hi<F>(raw, sc);
 #pragma unroll
-          for (int k = 0; k < D / 64; k++) {
-            const int at = (4 * g + e) * (D / 16) + 4 * k;  // dims at .. at + 3
-            const uint32_t raw = *(const uint32_t*)(lds + St::V_AT + tok * St::VP + at);
-            const float sc = e8m0(lds[St::VS_AT + tok * St::SP + at / 32]);
-            const uint32_t a = cvt_lo<F>(raw, sc), b = cvt_hi<F>(raw, sc);
-#pragma unroll
-            for (int d = 0; d < 4; d++) {
-              const uint32_t h = d < 2 ? a : b;
-              const float v = __builtin_bit_cast(float, d & 1 ? h & 0xFFFF0000u : h << 16);
-              sum.o[n][4 * k + d][e] = __builtin_fmaf(pt, v, sum.o[n][4 * k + d][e]);
-            }
+          for (int d = 0; d < 4; d++) {
+            const uint32_t h = d < 2 ? a : b;
+            const float v = __builtin_bit_cast(float, d & 1 ? h & 0xFFFF0000u : h << 16);
+            sum.o[0][4 * k + d][e] = __builtin_fmaf(pt, v, sum.o[0][4 * k + d][e]);
           }
-      }
+        }
     }
     return;
   }
@@ -394,55 +403,39 @@ __device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[D / 32
 #pragma unroll
     for (int d = 0; d < 4; d++) {
       const bf16x8 v = operand(w[d][0], w[d][1], w[d][2], w[d][3]);
-#pragma unroll
-      for (int n = 0; n < NR; n++)
-        sum.o[n][4 * k + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[n], sum.o[n][4 * k + d], 0, 0, 0);
+      sum.o[0][4 * k + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[0], sum.o[0][4 * k + d], 0, 0, 0);
     }
   }
 }
 
-template <int D, int F, int NR, int WAVES, int OCC>
+template <int D, int F, int WAVES, int OCC>
 __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
-  __shared__ float ml[WAVES][NR][16][2];
+  __shared__ float ml[WAVES][16][2];
   // the waves' staged tokens, then their outputs
   constexpr int OS = 4 * 16 * (D + 4), PIECE = Stage<D>::BYTES > OS ? Stage<D>::BYTES : OS;
   __shared__ __align__(16) uint8_t lds[WAVES * PIECE];
   float(*os)[16][D + 4] = (float(*)[16][D + 4])lds;
-  __shared__ bf16x8 q[NR][D / 32][64];  // by lane, the same for every wave
+  __shared__ bf16x8 q[D / 32][64];  // by lane, the same for every wave
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x, head = blockIdx.z % p.a.c.heads, b = blockIdx.z / p.a.c.heads;
-  const int row0 = blockIdx.y * (16 * NR);
+  const int split = blockIdx.x, head = blockIdx.y % p.a.c.heads, b = blockIdx.y / p.a.c.heads;
   const int32_t* table = p.a.table + (int64_t)b * p.a.ld_table;
   int len = p.a.lens[b];
   len = len < 0 ? 0 : (int64_t)len > p.a.max_len ? (int)p.a.max_len : len;
-  // tokens that a row sees: rows past the last take the last one's
-  auto limit_of = [&](int row) {
-    row = row < p.rows ? row : p.rows - 1;
-    return len - p.a.Lq + 1 + row / p.a.group;
-  };
-  int lim[NR], end = limit_of(row0 + 16 * NR - 1);
-  const int low = limit_of(row0);
-#pragma unroll
-  for (int n = 0; n < NR; n++) lim[n] = limit_of(row0 + 16 * n + i);
+  const int row = i < p.rows ? i : p.rows - 1;  // lanes past the last row repeat it
+  const int qt = row / p.a.group, hq = head * p.a.group + row - qt * p.a.group;
+  const int low = len - p.a.Lq + 1, lim = low + qt, end = low + (p.rows - 1) / p.a.group;  // tokens that rows see
   int t0 = split * p.chunk, t1 = t0 + p.chunk;
   if (t1 > end) t1 = end;
   if (split > 0 && t0 >= t1) return;  // the whole workgroup: no such piece of this request
 
-  const int heads_q = p.a.c.heads * p.a.group;
-  Sums<D, NR> sum;
+  Sums<D, 1> sum;
+  const uint16_t* src = p.a.q + ((int64_t)b * p.a.Lq + qt) * p.a.ld_q + (int64_t)hq * D + g * (D / 4);
+  for (int j = wave; j < D / 32; j += WAVES) q[j][lane] = *(const bf16x8*)(src + 8 * j);
+  sum.m[0] = -__builtin_inff();
+  sum.l[0] = 0.0f;
 #pragma unroll
-  for (int n = 0; n < NR; n++) {
-    int row = row0 + 16 * n + i;
-    row = row < p.rows ? row : p.rows - 1;
-    const int qt = row / p.a.group, hq = head * p.a.group + row - qt * p.a.group;
-    const uint16_t* src = p.a.q + ((int64_t)b * p.a.Lq + qt) * p.a.ld_q + (int64_t)hq * D + g * (D / 4);
-    for (int j = wave; j < D / 32; j += WAVES) q[n][j][lane] = *(const bf16x8*)(src + 8 * j);
-    sum.m[n] = -__builtin_inff();
-    sum.l[n] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < D / 16; d++) sum.o[n][d] = f32x4{0, 0, 0, 0};
-  }
+  for (int d = 0; d < D / 16; d++) sum.o[0][d] = f32x4{0, 0, 0, 0};
   __syncthreads();
   const float scale2 = p.a.scale * 1.44269504088896340736f;  // scores in units of log 2
 
@@ -450,18 +443,20 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
   if (t < t1) {
     uint8_t* mine = lds + wave * Stage<D>::BYTES;
     Raw<D> x;
-    uint32_t there = load_step<D>(p, table, head, t, t1, x);
+    constexpr int STRIDE = WAVES * STEP;
+    uint32_t there = load_step<D>(p, page_of(p, table, t, t1), head, t, x);
+    int pages = page_of(p, table, t + STRIDE, t1);
     while (true) {
       const bool cut = there != 3u || t + STEP > low;
       const uint32_t here = there;
       const bool odd = __any(stage_step<D, F>(x, mine, cut, here, t1 - t)) && p.a.Lq > 1;
       wave_fence();
-      const int next = t + WAVES * STEP;
-      if (next < t1) there = load_step<D>(p, table, head, next, t1, x);
-      int limit[NR];
-#pragma unroll
-      for (int n = 0; n < NR; n++) limit[n] = lim[n] - t;
-      take_step<D, F, NR>(mine, q, scale2, cut, odd, here, limit, sum);
+      const int next = t + STRIDE;
+      if (next < t1) {
+        there = load_step<D>(p, pages, head, next, x);
+        pages = page_of(p, table, next + STRIDE, t1);
+      }
+      take_step<D, F>(mine, q, scale2, cut, odd, here, lim - t, sum);
       wave_fence();
       t = next;
       if (t >= t1) break;
@@ -469,58 +464,375 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
   }
 
   // join the waves
+  sum.l[0] = rows_sum(sum.l[0]);
+  if (g == 0) {
+    ml[wave][i][0] = sum.m[0];
+    ml[wave][i][1] = sum.l[0];
+  }
+  __syncthreads();  // the staged tokens' place holds outputs now
+  float m = -__builtin_inff();
 #pragma unroll
-  for (int n = 0; n < NR; n++) {
-    sum.l[n] = rows_sum(sum.l[n]);
-    if (g == 0) {
-      ml[wave][n][i][0] = sum.m[n];
-      ml[wave][n][i][1] = sum.l[n];
+  for (int w = 0; w < WAVES; w++) m = __builtin_fmaxf(m, ml[w][i][0]);
+  const float a = __builtin_amdgcn_exp2f(sum.m[0] - (m == -__builtin_inff() ? 0.0f : m));
+#pragma unroll
+  for (int d = 0; d < D / 16; d++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) os[wave][i][(4 * g + e) * (D / 16) + d] = sum.o[0][d][e] * a;
+  __syncthreads();
+  for (int at = threadIdx.x; at < p.rows * D; at += 64 * WAVES) {
+    const int r = at / D, d = at % D;
+    float mm = -__builtin_inff(), l = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) mm = __builtin_fmaxf(mm, ml[w][r][0]);
+    const float base = mm == -__builtin_inff() ? 0.0f : mm;
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) {
+      l += ml[w][r][1] * __builtin_amdgcn_exp2f(ml[w][r][0] - base);
+      o += os[w][r][d];
+    }
+    if (p.splits == 1) {
+      const int rt = r / p.a.group;
+      const int64_t tok = (int64_t)b * p.a.Lq + rt, hr = head * p.a.group + r - rt * p.a.group;
+      const bool none = l == 0.0f;  // the row sees no token (the largest score's own p is not 0)
+      p.a.o[tok * p.a.ld_o + hr * D + d] = __builtin_bit_cast(uint16_t, (__bf16)(none ? 0.0f : o / l));
+      if (d == 0 && p.a.lse)
+        p.a.lse[tok * (p.a.c.heads * p.a.group) + hr] =
+            none ? -__builtin_inff() : mm * 0.69314718055994530942f + logf(l);
+    } else {
+      const int64_t part = (((int64_t)b * p.a.c.heads + head) * p.rows + r) * p.splits + split;
+      p.part_o[part * D + d] = o;
+      if (d == 0) {
+        p.part_ml[2 * part] = mm;
+        p.part_ml[2 * part + 1] = l;
+      }
     }
   }
-  __syncthreads();
+}
+
+// Many rows: the waves of a workgroup take 16 NR rows each and share the tokens, 32
+// at a time, so a token is converted once for 64 NR rows.  The workgroup converts
+// its tokens to bf16 into LDS, in two buffers by turns (one barrier a step), while
+// the next ones are on their way:
+//   K  [token][dims], 16 more bytes a row
+//   V  [dim][token] with the dims that a lane holds (4 c .. 4 c + 3) D/4 rows apart
+//      (row_of), tokens in the order of the second product's lanes (8 g + 4 u + r for
+//      token 16 u + 4 g + r), and the four 16-byte pieces of a row exchanged by row, so
+//      that both the writes and the reads spread over the banks
+// Bound: matrix and softmax instructions of the waves and LDS reads (16 KB a wave and
+// step for D = 128) alike.
+template <int D>
+struct Shared {
+  static constexpr int KP = 2 * D + 16, K_BYTES = 32 * KP, BYTES = K_BYTES + D * 64;
+  static constexpr int KL = D <= 128 ? 1 : D / 128;           // 16-byte pieces of K in a lane
+  static constexpr int VL = KL;                               // 4 x 4 pieces of V in a lane
+  static constexpr int USED = D < 128 ? 2 * D : 256;          // lanes that hold pieces
+  __device__ static int v_at(int row, int piece) { return K_BYTES + row * 64 + ((piece ^ (row >> 2)) & 3) * 16; }
+};
+template <int D>
+struct Tokens {
+  u32x4 k[Shared<D>::KL];
+  uint32_t ks[Shared<D>::KL];
+  uint32_t v[Shared<D>::VL][4], vs[Shared<D>::VL][D / 32];
+};
+
+template <int D>
+__device__ __forceinline__ uint32_t load_tokens(const AttnArgs& p, int pages, int head, int t0,
+                                                Tokens<D>& x) {
+  const int tid = threadIdx.x;
+  uint32_t there = 0;
+  int64_t row[2];
+#pragma unroll
+  for (int u = 0; u < 2; u++) {
+    const bool ok = locate(p, pages, head, t0, u, row[u]);
+    there |= (uint32_t)ok << u;
+  }
+  if (Shared<D>::USED < 256 && tid >= Shared<D>::USED) return there;
+#pragma unroll
+  for (int c = 0; c < Shared<D>::KL; c++) {
+    const int f = tid + 256 * c, tok = f / (D / 16), at = f % (D / 16);
+    const int64_t r = (tok < 16 ? row[0] : row[1]) + (tok & 15);
+    x.k[c] = *(const u32x4*)(p.a.c.k_q + r * D + 16 * at);
+    x.ks[c] = p.a.c.k_s[r * (D / 32) + at / 2];
+    const int quad = f / (D / 4), dc = f % (D / 4);  // tokens 4 quad .., dims 4 dc ..
+    const int64_t rv = (quad < 4 ? row[0] : row[1]) + 4 * (quad & 3);
+#pragma unroll
+    for (int r4 = 0; r4 < 4; r4++) x.v[c][r4] = *(const uint32_t*)(p.a.c.v_q + (rv + r4) * D + 4 * dc);
+    load_words<D / 32>(p.a.c.v_s + rv * (D / 32), x.vs[c]);
+  }
+  return there;
+}
+
+// Converted into a buffer; tokens that are cut are zeros (stage_step says why).  True
+// where another value may not be finite (asked only with `cut`).
+template <int D, int F>
+__device__ __forceinline__ bool stage_tokens(const Tokens<D>& x, uint8_t* buf, bool cut, uint32_t there, int end) {
+  using Sh = Shared<D>;
+  const int tid = threadIdx.x;
+  bool odd = false;
+  if (Sh::USED < 256 && tid >= Sh::USED) return odd;
+#pragma unroll
+  for (int c = 0; c < Sh::KL; c++) {
+    const int f = tid + 256 * c;
+    const float ks = e8m0(x.ks[c]);
+    uint8_t* kd = buf + f / (D / 16) * Sh::KP + f % (D / 16) * 32;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const uint32_t w0 = x.k[c][2 * h], w1 = x.k[c][2 * h + 1];
+      *(u32x4*)(kd + 16 * h) = u32x4{cvt_lo<F>(w0, ks), cvt_hi<F>(w0, ks), cvt_lo<F>(w1, ks), cvt_hi<F>(w1, ks)};
+    }
+    const int quad = f / (D / 4), dc = f % (D / 4), blk = dc / 8;
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      // byte r D/32 + blk of x.vs[c]
+      uint32_t code, raw = x.v[c][r];
+      if constexpr (D == 64) code = (x.vs[c][r >> 1] >> (16 * (r & 1) + 8 * blk)) & 0xFFu;
+      else if constexpr (D == 128) code = (x.vs[c][r] >> (8 * blk)) & 0xFFu;
+      else code = ((blk & 4 ? x.vs[c][2 * r + 1] : x.vs[c][2 * r]) >> (8 * (blk & 3))) & 0xFFu;
+      if (cut) {
+        const bool gone = !(there >> (quad >> 2) & 1) || 4 * quad + r >= end;
+        code = gone ? 127u : code;
+        raw = gone ? 0u : raw;
+        odd |= (((raw & 0x7F7F7F7Fu) + (F == E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u) != 0 ||
+               code > (uint32_t)(254 - Fmt<F>::emax);
+      }
+      lo[r] = cvt_lo<F>(raw, e8m0(code));
+      hi[r] = cvt_hi<F>(raw, e8m0(code));
+    }
+    const int piece = quad & 3, half = 8 * (quad >> 2);
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const uint32_t* w = e < 2 ? lo : hi;
+      const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+      *(uint2*)(buf + Sh::v_at(e * (D / 4) + dc, piece) + half) =
+          make_uint2(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel));
+    }
+  }
+  return odd;
+}
+
+// Outputs of the 16 rows from row0 on.  ND pieces of the sums as the second product
+// leaves them (piece d0 + d of row l % 16), divided by the row's l, go to `os`, 16
+// (D + 2) bf16 of LDS; `count` waves then store the rows, this one from `first` on.
+template <int D, int ND>
+__device__ __forceinline__ void put_rows(const f32x4 (&o)[ND], int d0, float l, uint16_t* os) {
+  const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // l = 0: the row sees no token
+#pragma unroll
+  for (int d = 0; d < ND; d++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const int r = 16 * (d0 + d) + 4 * g + e;  // row of V's buffer: dim 4 (r % (D / 4)) + r / (D / 4)
+      os[i * (D + 2) + 4 * (r % (D / 4)) + r / (D / 4)] = __builtin_bit_cast(uint16_t, (__bf16)(o[d][e] * inv));
+    }
+}
+template <int D>
+__device__ __forceinline__ void store_rows(const AttnArgs& p, int b, int head, int row0, float l, float m,
+                                           const uint16_t* os, int first, int count) {
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int row = row0 + i, qt = row / p.a.group, hq = head * p.a.group + row - qt * p.a.group;
+  if (first == 0 && g == 0 && row < p.rows && p.a.lse)
+    p.a.lse[((int64_t)b * p.a.Lq + qt) * (p.a.c.heads * p.a.group) + hq] =
+        l == 0.0f ? -__builtin_inff() : m * 0.69314718055994530942f + logf(l);
+#pragma unroll 4
+  for (int r = first; r < 16; r += count) {
+    if (row0 + r >= p.rows) break;
+    const int64_t tok = (int64_t)b * p.a.Lq + __builtin_amdgcn_readlane(qt, r);
+    uint16_t* to = p.a.o + tok * p.a.ld_o + (int64_t)__builtin_amdgcn_readlane(hq, r) * D;
+#pragma unroll
+    for (int k = 0; k < D / 64; k++) to[64 * k + lane] = os[r * (D + 2) + 64 * k + lane];
+  }
+}
+
+template <int D, int F, int NR>
+__global__ __launch_bounds__(256, 2) void k_attention_rows(AttnArgs p) {
+  using Sh = Shared<D>;
+  constexpr int OS = 16 * (D + 2) * 2;  // bytes of a wave's 16 rows of outputs
+  static_assert(2 * Sh::BYTES >= 4 * OS, "outputs fit into the buffers");
+  __shared__ __align__(16) uint8_t lds[2 * Sh::BYTES];
+  __shared__ __align__(16) uint16_t ps[4][16][32];
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x, head = blockIdx.y % p.a.c.heads, b = blockIdx.y / p.a.c.heads;
+  // the last rows see most tokens: their workgroups begin first
+  const int wg0 = (int)(gridDim.z - 1 - blockIdx.z) * (64 * NR), row0 = wg0 + wave * (16 * NR);
+  const int32_t* table = p.a.table + (int64_t)b * p.a.ld_table;
+  int len = p.a.lens[b];
+  len = len < 0 ? 0 : (int64_t)len > p.a.max_len ? (int)p.a.max_len : len;
+  auto limit_of = [&](int row) {  // tokens that a row sees: rows past the last take the last one's
+    row = row < p.rows ? row : p.rows - 1;
+    return len - p.a.Lq + 1 + row / p.a.group;
+  };
+  int t0 = split * p.chunk, t1 = t0 + p.chunk;
+  const int end = limit_of(wg0 + 64 * NR - 1);
+  if (t1 > end) t1 = end;
+  if (split > 0 && t0 >= t1) return;  // the whole workgroup: no such piece of this request
+  const int low = limit_of(wg0), wave_low = limit_of(row0), wave_end = limit_of(row0 + 16 * NR - 1);
+  const bool idle = row0 >= p.rows;
+
+  bf16x8 q[NR][D / 32];
+  Sums<D, NR> sum;
+  int lim[NR];
 #pragma unroll
   for (int n = 0; n < NR; n++) {
-    float m = -__builtin_inff();
+    int row = row0 + 16 * n + i;
+    lim[n] = limit_of(row);
+    row = row < p.rows ? row : p.rows - 1;
+    const int qt = row / p.a.group, hq = head * p.a.group + row - qt * p.a.group;
+    const uint16_t* src = p.a.q + ((int64_t)b * p.a.Lq + qt) * p.a.ld_q + (int64_t)hq * D + 8 * g;
 #pragma unroll
-    for (int w = 0; w < WAVES; w++) m = __builtin_fmaxf(m, ml[w][n][i][0]);
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-    const float a = __builtin_amdgcn_exp2f(sum.m[n] - base);
+    for (int j = 0; j < D / 32; j++) q[n][j] = *(const bf16x8*)(src + 32 * j);
+    sum.m[n] = -__builtin_inff();
+    sum.l[n] = 0.0f;
 #pragma unroll
-    for (int d = 0; d < D / 16; d++)
+    for (int d = 0; d < D / 16; d++) sum.o[n][d] = f32x4{0, 0, 0, 0};
+  }
+  const float scale2 = p.a.scale * 1.44269504088896340736f;  // scores in units of log 2
+
+  Tokens<D> x;
+  uint32_t there = 0;
+  int pages = -1;
+  if (t0 < t1) {
+    there = load_tokens<D>(p, page_of(p, table, t0, t1), head, t0, x);
+    pages = page_of(p, table, t0 + STEP, t1);
+  }
+  for (int t = t0, turn = 0; t < t1; t += STEP, turn ^= 1) {
+    uint8_t* buf = lds + turn * Sh::BYTES;
+    const uint32_t here = there;
+    const bool wg_cut = here != 3u || t + STEP > low;
+    bool odd = stage_tokens<D, F>(x, buf, wg_cut, here, t1 - t);
+    if (wg_cut) odd = __syncthreads_or(odd) != 0;
+    else __syncthreads();
+    if (t + STEP < t1) {
+      there = load_tokens<D>(p, pages, head, t + STEP, x);
+      pages = page_of(p, table, t + 2 * STEP, t1);
+    }
+    if (idle || t >= wave_end) continue;
+    f32x4 s[NR][2];
 #pragma unroll
-      for (int e = 0; e < 4; e++) os[wave][i][(4 * g + e) * (D / 16) + d] = sum.o[n][d][e] * a;
-    __syncthreads();
-    for (int at = threadIdx.x; at < 16 * D; at += 64 * WAVES) {
-      const int r = at / D, d = at % D, row = row0 + 16 * n + r;
-      if (row >= p.rows) break;  // later ones are past the last row too
-      float mm = -__builtin_inff(), l = 0.0f, o = 0.0f;
+    for (int n = 0; n < NR; n++) s[n][0] = s[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < WAVES; w++) mm = __builtin_fmaxf(mm, ml[w][n][r][0]);
-      const float bb = mm == -__builtin_inff() ? 0.0f : mm;
+    for (int j = 0; j < D / 32; j++)
 #pragma unroll
-      for (int w = 0; w < WAVES; w++) {
-        l += ml[w][n][r][1] * __builtin_amdgcn_exp2f(ml[w][n][r][0] - bb);
-        o += os[w][r][d];
+      for (int u = 0; u < 2; u++) {
+        const bf16x8 k = *(const bf16x8*)(buf + (16 * u + i) * Sh::KP + 64 * j + 16 * g);
+#pragma unroll
+        for (int n = 0; n < NR; n++) s[n][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[n][j], s[n][u], 0, 0, 0);
       }
-      const int qt = row / p.a.group, hq = head * p.a.group + row - qt * p.a.group;
-      if (p.splits == 1) {
-        const int64_t tok = (int64_t)b * p.a.Lq + qt;
-        const bool none = l == 0.0f;  // the row sees no token (the largest score's own p is 1)
-        const float v = none ? 0.0f : o / l;
-        p.a.o[tok * p.a.ld_o + (int64_t)hq * D + d] = __builtin_bit_cast(uint16_t, (__bf16)v);
-        if (d == 0 && p.a.lse)
-          p.a.lse[tok * heads_q + hq] = none ? -__builtin_inff() : mm * 0.69314718055994530942f + logf(l);
-      } else {
-        const int64_t part = (((int64_t)b * p.a.c.heads + head) * p.rows + row) * p.splits + split;
-        p.part_o[part * D + d] = o;
-        if (d == 0) {
-          p.part_ml[2 * part] = mm;
-          p.part_ml[2 * part + 1] = l;
+#pragma unroll
+    for (int n = 0; n < NR; n++)
+#pragma unroll
+      for (int u = 0; u < 2; u++) s[n][u] *= scale2;
+    if (here != 3u || t + STEP > wave_low) {
+#pragma unroll
+      for (int n = 0; n < NR; n++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const int tok = 16 * (e >> 2) + 4 * g + (e & 3);
+          const bool seen = tok < lim[n] - t && (here >> (e >> 2) & 1);
+          s[n][e >> 2][e & 3] = seen ? s[n][e >> 2][e & 3] : -__builtin_inff();
+        }
+    }
+    bf16x8 pr[NR];
+    soften<D, NR>(s, sum, pr);
+    if (odd && p.a.Lq > 1) {
+      // 0 * NaN is not 0: token by token, for the rows that see it
+#pragma unroll
+      for (int n = 0; n < NR; n++) {
+        wave_fence();
+        *(uint2*)&ps[wave][i][4 * g] = __builtin_bit_cast(u64x2, pr[n]).lo;
+        *(uint2*)&ps[wave][i][16 + 4 * g] = __builtin_bit_cast(u64x2, pr[n]).hi;
+        wave_fence();
+        for (int tok = 0; tok < STEP; tok++) {
+          if (tok >= lim[n] - t) continue;
+          const float pt = __builtin_bit_cast(float, (uint32_t)ps[wave][i][tok] << 16);
+#pragma unroll
+          for (int d = 0; d < D / 16; d++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const uint16_t v = *(const uint16_t*)(buf + Sh::v_at(16 * d + 4 * g + e, (tok & 15) >> 2) +
+                                                    8 * (tok >> 4) + 2 * (tok & 3));
+              sum.o[n][d][e] = __builtin_fmaf(pt, __builtin_bit_cast(float, (uint32_t)v << 16), sum.o[n][d][e]);
+            }
         }
       }
+      continue;
     }
-    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < D / 16; d++) {
+      const bf16x8 v = *(const bf16x8*)(buf + Sh::v_at(16 * d + i, g));
+#pragma unroll
+      for (int n = 0; n < NR; n++)
+        sum.o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[n], sum.o[n][d], 0, 0, 0);
+    }
   }
+  __syncthreads();  // the buffers hold outputs now
+  if (idle) return;
+#pragma unroll
+  for (int n = 0; n < NR; n++) {
+    const float l = rows_sum(sum.l[n]);
+    const int r0 = row0 + 16 * n;
+    if (r0 >= p.rows) break;
+    if (p.splits == 1) {
+      uint16_t* os = (uint16_t*)(lds + wave * OS);
+      wave_fence();
+      put_rows<D, D / 16>(sum.o[n], 0, l, os);
+      wave_fence();
+      store_rows<D>(p, b, head, r0, l, sum.m[n], os, 0, 1);
+    } else {  // as they are held, 1 KB at a time
+      const int64_t part = (((int64_t)b * p.a.c.heads + head) * ((p.rows + 15) / 16) + r0 / 16) * p.splits + split;
+#pragma unroll
+      for (int d = 0; d < D / 16; d++) *(f32x4*)(p.part_o + (part * (D / 16) + d) * 256 + 4 * lane) = sum.o[n][d];
+      if (g == 0) *(f32x2*)(p.part_ml + (part * 16 + i) * 2) = f32x2{sum.m[n], l};
+    }
+  }
+}
+
+// Joins the pieces of 16 rows; each wave a quarter of their dims.
+template <int D>
+__global__ __launch_bounds__(256) void k_attention_join_rows(AttnArgs p) {
+  constexpr int ND = D / 64;
+  __shared__ uint16_t os[16 * (D + 2)];
+  const int lane = threadIdx.x & 63, i = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = (p.rows + 15) / 16;
+  const int64_t at = blockIdx.x;
+  const int row0 = (int)(at % tiles) * 16;
+  const int64_t bh = at / tiles;
+  const int head = (int)(bh % p.a.c.heads), b = (int)(bh / p.a.c.heads);
+  int len = p.a.lens[b];
+  len = len < 0 ? 0 : (int64_t)len > p.a.max_len ? (int)p.a.max_len : len;
+  // the pieces that hold tokens of the lane's row, which have all been computed
+  auto pieces = [&](int row) {
+    const int limit = len - p.a.Lq + 1 + (row < p.rows ? row : p.rows - 1) / p.a.group;
+    return limit <= 0 ? 0 : (limit + p.chunk - 1) / p.chunk;
+  };
+  const int mine = pieces(row0 + i), most = pieces(row0 + 15);
+  const float* ml = p.part_ml + at * p.splits * 32 + 2 * i;
+  const float* po = p.part_o + (at * p.splits * (D / 16) + wave * ND) * 256 + 4 * lane;
+  float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < mine; s++) m = __builtin_fmaxf(m, ml[32 * s]);
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+  f32x4 o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; d++) o[d] = f32x4{0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < most; s++) {
+    f32x4 part[ND];
+#pragma unroll
+    for (int d = 0; d < ND; d++) part[d] = *(const f32x4*)(po + ((int64_t)s * (D / 16) + d) * 256);
+    const f32x2 w = s < mine ? *(const f32x2*)(ml + 32 * s) : f32x2{-__builtin_inff(), 0.0f};
+    const float a = __builtin_amdgcn_exp2f(w.x - base);
+    l += w.y * a;
+#pragma unroll
+    for (int d = 0; d < ND; d++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[d][e] = s < mine ? __builtin_fmaf(part[d][e], a, o[d][e]) : o[d][e];
+  }
+  put_rows<D, ND>(o, wave * ND, l, os);
+  __syncthreads();
+  store_rows<D>(p, b, head, row0, l, m, os, wave, 4);
 }
 
 // Joins the pieces of a row.  W waves of a workgroup take a row, each of them every
@@ -580,28 +892,31 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs p) {
         l == 0.0f ? -__builtin_inff() : m * 0.69314718055994530942f + logf(l);
 }
 
-// Row tiles and waves of a workgroup, and how the tokens are split: by sizes that
-// the host knows, so a result does not depend on timing.
+// Shape of the workgroups, and how the tokens are split: by sizes that the host knows,
+// so a result does not depend on timing.
 struct Plan {
+  bool shared;  // more than 16 rows: k_attention_rows
   int nr, waves, tiles, splits, chunk;
 };
-// More tiles share the conversion of the tokens, as far as registers go without
-// spilling (dim 128: two; four ran 60 us against 38 us for 4 requests of 64 query
-// tokens to 4096).  Workgroups are wanted twice for each that the chip holds at a
-// time (two of four waves a CU, one for dim 256), which evens out requests of
-// different lengths: 32 requests to 16384, dim 128, took 136 us in 4 pieces, 143 in
-// 16.  Up to 1024 tokens of few rows eight waves of one workgroup spare the second
-// launch.
+// Up to 16 rows the waves of a workgroup take tokens by turns; more rows are shared
+// out to them (8 requests to 4096, 8 heads of dim 128: 16 rows 21.6 us by tokens and
+// 22.1 by rows, 32 rows 29.4 and 24.0, 64 rows 35 and 27).  Workgroups are wanted
+// twice for each that the chip holds at a time (two of four waves a CU, one for dim
+// 256), which evens out requests of different lengths: 32 requests to 16384, dim 128,
+// took 136 us in 4 pieces, 143 in 16.  Up to 1024 tokens of few rows eight waves of
+// one workgroup spare the second launch.
 Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_len) {
   Plan r;
   const int64_t rows = Lq * group;
-  r.nr = rows <= 16 || dim == 256 ? 1 : rows <= 32 || dim == 128 ? 2 : 4;
-  r.waves = r.nr == 1 && dim < 256 && max_len <= 1024 ? 8 : 4;
-  r.tiles = (int)((rows + 16 * r.nr - 1) / (16 * r.nr));
-  const int64_t unit = STEP * r.waves, base = B * heads * r.tiles, want = dim == 256 ? 512 : 1024;
+  r.shared = rows > 16;
+  r.nr = rows > 64 && dim < 256 ? 2 : 1;
+  r.waves = !r.shared && dim < 256 && max_len <= 1024 ? 8 : 4;
+  r.tiles = r.shared ? (int)((rows + 64 * r.nr - 1) / (64 * r.nr)) : 1;
+  const int64_t unit = r.shared ? 128 : STEP * r.waves, base = B * heads * r.tiles;
   const int64_t units = (max_len + unit - 1) / unit;
-  int64_t splits = r.waves == 8 ? 1 : (want + base - 1) / base;
+  int64_t splits = r.waves == 8 ? 1 : ((!r.shared && dim == 256 ? 512 : 1024) + base - 1) / base;
   if (splits > (units + 1) / 2) splits = (units + 1) / 2;  // at least two steps a wave
+  if (r.shared && splits > 16) splits = 16;                // joining them costs a row's outputs each
   if (splits < 1) splits = 1;
   int64_t per = (units + splits - 1) / splits;
   if (per < 1) per = 1;
@@ -613,20 +928,28 @@ Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_l
 
 template <int D, int F>
 hipError_t attention_by_rows(const AttnArgs& p, const Plan& r, hipStream_t st) {
-  const dim3 g((unsigned)r.splits, (unsigned)r.tiles, (unsigned)(p.a.B * p.a.c.heads)), b(64 * r.waves);
+  const unsigned bh = (unsigned)(p.a.B * p.a.c.heads);
+  const dim3 b(64 * r.waves), b4(256);
+  if (r.shared) {
+    const dim3 g((unsigned)r.splits, bh, (unsigned)r.tiles);
+    if (r.nr == 1) hipLaunchKernelGGL((k_attention_rows<D, F, 1>), g, b, 0, st, p);
+    if constexpr (D < 256)
+      if (r.nr == 2) hipLaunchKernelGGL((k_attention_rows<D, F, 2>), g, b, 0, st, p);
+    if (r.splits > 1)
+      hipLaunchKernelGGL(k_attention_join_rows<D>, dim3(bh * (unsigned)((p.rows + 15) / 16)), b4, 0, st, p);
+    return hipGetLastError();
+  }
+  const dim3 g((unsigned)r.splits, bh);
   if constexpr (D == 256) {
-    hipLaunchKernelGGL((k_attention<D, F, 1, 4, 1>), g, b, 0, st, p);
+    hipLaunchKernelGGL((k_attention<D, F, 4, 1>), g, b, 0, st, p);
   } else {
-    if (r.waves == 8) hipLaunchKernelGGL((k_attention<D, F, 1, 8, 2>), g, b, 0, st, p);
-    else if (r.nr == 1) hipLaunchKernelGGL((k_attention<D, F, 1, 4, 2>), g, b, 0, st, p);
-    else if (r.nr == 2) hipLaunchKernelGGL((k_attention<D, F, 2, 4, 2>), g, b, 0, st, p);
-    if constexpr (D == 64)
-      if (r.nr == 4) hipLaunchKernelGGL((k_attention<D, F, 4, 4, 2>), g, b, 0, st, p);
+    if (r.waves == 8) hipLaunchKernelGGL((k_attention<D, F, 8, 2>), g, b, 0, st, p);
+    else hipLaunchKernelGGL((k_attention<D, F, 4, 2>), g, b, 0, st, p);
   }
   if (r.splits > 1) {  // 8192 rows: 12 us by four waves each, 6 by one; 32 rows of 64 pieces: 5 us and 20
-    const int64_t n = (int64_t)p.a.B * p.a.c.heads * p.rows;
-    if (n >= 2048) hipLaunchKernelGGL((k_attention_join<D, 1>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((k_attention_join<D, 4>), dim3((unsigned)n), dim3(256), 0, st, p);
+    const unsigned n = bh * (unsigned)p.rows;
+    if (n >= 2048) hipLaunchKernelGGL((k_attention_join<D, 1>), dim3((n + 3) / 4), b4, 0, st, p);
+    else hipLaunchKernelGGL((k_attention_join<D, 4>), dim3(n), b4, 0, st, p);
   }
   return hipGetLastError();
 }
@@ -654,7 +977,8 @@ hipError_t launch_cache_write(const CacheWriteArgs& a, hipStream_t st) {
 
 int64_t attention_workspace(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_len) {
   const Plan r = plan_of(B, Lq, heads, group, dim, max_len);
-  return r.splits == 1 ? 0 : B * heads * Lq * group * r.splits * (dim + 2) * 4;
+  const int64_t rows = r.shared ? (Lq * group + 15) / 16 * 16 : Lq * group;  // whole tiles
+  return r.splits == 1 ? 0 : B * heads * rows * r.splits * (dim + 2) * 4;
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t st) {
@@ -667,7 +991,8 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t st) {
   p.page16 = (uint32_t)a.c.page / 16;
   p.magic = p.page16 > 1 ? (uint32_t)(((1ull << 32) + p.page16 - 1) / p.page16) : 0;
   p.part_o = a.work;
-  p.part_ml = a.work + (int64_t)a.B * a.c.heads * p.rows * r.splits * a.c.dim;
+  const int64_t rows = r.shared ? (p.rows + 15) / 16 * 16 : p.rows;
+  p.part_ml = a.work + (int64_t)a.B * a.c.heads * rows * r.splits * a.c.dim;
   switch (a.c.dim) {
     case 64: return attention_by_fmt<64>(p, r, st);
     case 128: return attention_by_fmt<128>(p, r, st);

@@ -235,8 +235,9 @@ int mx_rmsnorm_quantize(const void* x, int64_t ld_x, const void* r, int64_t ld_r
  *   dh      the gradient that reaches h another way (the residual stream), or NULL.
  *   dx      [rows x cols] of type src; may be dy or dh.
  *   dw      [cols] fp32, overwritten; its sums are taken in a fixed order.
- *   workspace  mx_rmsnorm_backward_workspace(rows, cols, src) bytes, 16-byte
- *           aligned, in use until the call's work is done.  MX_ERR_SHAPE if smaller.
+ *   workspace  mx_rmsnorm_backward_workspace(rows, cols, src) bytes (may be 0),
+ *           16-byte aligned, in use until the call's work is done.  MX_ERR_SHAPE if
+ *           smaller.
  * Alignment and sizes as for mx_rmsnorm_quantize.  rows == 0 writes zeros to dw.
  */
 int mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* w,

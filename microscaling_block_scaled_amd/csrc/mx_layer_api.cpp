@@ -132,7 +132,8 @@ int mx_rmsnorm_quantize(const void* x, int64_t ld_x, const void* r, int64_t ld_r
 
 int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int32_t src) {
   if (!src_ok(src) || rows < 0 || cols < 0 || rows >= kMaxRows || cols > kMaxNormCols) return -1;
-  return mx::norm_grad_partials(rows, cols, src) * cols * 4;
+  const int64_t n = mx::norm_grad_partials(rows, cols, src);
+  return n > 1 ? n * cols * 4 : 0;
 }
 
 int mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* w,
@@ -146,13 +147,18 @@ int mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld
   if (!aligned(dw, 4)) return MX_ERR_ALIGN;
   const int64_t esz = esz_of(src);
   if (rows > 0) {
-    if (!dy || !h || !w || !rstd || !dx || !workspace) return MX_ERR_ARG;
+    if (!dy || !h || !w || !rstd || !dx) return MX_ERR_ARG;
     const void* p[] = {dy, h, dh, dx};
     const int64_t ld[] = {ld_dy, ld_h, ld_dh, ld_dx};
     for (int i = 0; i < 4; i++)
       if (const int e = check_rows(p[i], ld[i], cols, esz)) return e;
-    if (!aligned(w, 16) || !aligned(rstd, 4) || !aligned(workspace, 16)) return MX_ERR_ALIGN;
-    if (workspace_bytes < mx_rmsnorm_backward_workspace(rows, cols, src)) return MX_ERR_SHAPE;
+    if (!aligned(w, 16) || !aligned(rstd, 4)) return MX_ERR_ALIGN;
+    const int64_t need = mx_rmsnorm_backward_workspace(rows, cols, src);
+    if (need > 0) {
+      if (!workspace) return MX_ERR_ARG;
+      if (!aligned(workspace, 16)) return MX_ERR_ALIGN;
+      if (workspace_bytes < need) return MX_ERR_SHAPE;
+    }
   }
   mx::NormGradArgs a;
   a.dy = dy;

@@ -498,9 +498,10 @@ hipError_t norm_by_fmt(const NormArgs& a, hipStream_t st) {
 int grad_waves(int64_t cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : 8; }
 
 template <int SRC>
-hipError_t grad_launch(const NormGradArgs& a, hipStream_t st) {
+hipError_t grad_launch(NormGradArgs a, hipStream_t st) {
   const int64_t n = norm_grad_partials(a.rows, a.cols, SRC);
   const dim3 g((unsigned)n), b(WG);
+  if (n == 1) a.partial = a.dw;
   if (a.rows == 0) {  // dw is a sum of nothing
   } else if (a.cols > grad_max_cols(SRC)) {
     const dim3 gc((unsigned)((a.cols + 8 * WG - 1) / (8 * WG)), (unsigned)n);
@@ -514,8 +515,9 @@ hipError_t grad_launch(const NormGradArgs& a, hipStream_t st) {
     else if (a.cols <= 8192) hipLaunchKernelGGL((k_norm_grad<SRC, 8, 2>), g, b, 0, st, a);
     else if constexpr (SRC == SRC_BF16) hipLaunchKernelGGL((k_norm_grad<SRC, 8, 4>), g, b, 0, st, a);
   }
-  hipLaunchKernelGGL(k_sum_partials, dim3((unsigned)((a.cols + 63) / 64)), dim3(1024), 0, st,
-                     (const float*)a.partial, (int)n, a.cols, a.dw);
+  if (n != 1)  // a single workgroup's partial sums are dw
+    hipLaunchKernelGGL(k_sum_partials, dim3((unsigned)((a.cols + 63) / 64)), dim3(1024), 0, st,
+                       (const float*)a.partial, (int)n, a.cols, a.dw);
   return hipGetLastError();
 }
 

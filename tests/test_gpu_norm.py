@@ -231,7 +231,7 @@ def test_refusals(mx):
         mx.rmsnorm_quantize(x, w, mx.E4M3, eps=-1.0)
     assert err.value.status == mx.MX_ERR_ARG
     with pytest.raises(mx.MXError) as err:
-        mx.rmsnorm_backward(x, x, w, e(4, t=torch.float32), workspace=e(16, t=torch.uint8))
+        mx.rmsnorm_backward(e(40, 64), e(40, 64), w, e(40, t=torch.float32), workspace=e(16, t=torch.uint8))
     assert err.value.status == mx.MX_ERR_SHAPE
     with pytest.raises(ValueError):
         mx.rmsnorm_backward(x, x, w, e(3, t=torch.float32))

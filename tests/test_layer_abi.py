@@ -38,13 +38,14 @@ def test_rmsnorm_quantize_validation(mx):
 
 @no_gpu
 def test_rmsnorm_backward_validation(mx):
-    need = mx.lib.mx_rmsnorm_backward_workspace(4, 64, 1)
+    need = mx.lib.mx_rmsnorm_backward_workspace(40, 64, 1)
     assert need > 0 and need % (64 * 4) == 0
-    assert mx.lib.mx_rmsnorm_backward_workspace(0, 64, 1) == 0
+    for rows in (0, 1, 8):  # one workgroup needs none
+        assert mx.lib.mx_rmsnorm_backward_workspace(rows, 64, 1) == 0
     for bad in ((-1, 64, 1), (4, -1, 1), (4, 64, 2), (1 << 31, 64, 1), (4, 1 << 25, 1)):
         assert mx.lib.mx_rmsnorm_backward_workspace(*bad) == -1
 
-    def f(dy=FAKE, ld_dy=64, h=FAKE, ld_h=64, w=FAKE, rstd=FAKE, dh=FAKE, ld_dh=64, rows=4, cols=64, src=1, dx=FAKE,
+    def f(dy=FAKE, ld_dy=64, h=FAKE, ld_h=64, w=FAKE, rstd=FAKE, dh=FAKE, ld_dh=64, rows=40, cols=64, src=1, dx=FAKE,
           ld_dx=64, dw=FAKE, ws=FAKE, size=need):
         return mx.lib.mx_rmsnorm_backward(dy, ld_dy, h, ld_h, w, rstd, dh, ld_dh, rows, cols, src, dx, ld_dx, dw, ws,
                                           size, None)

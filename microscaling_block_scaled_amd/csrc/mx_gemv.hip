@@ -16,10 +16,11 @@
 // 8 j .. 8 j + 7 to instruction j; the tokens' lanes take the same elements of x,
 // which is all the order that a sum over k needs.
 //
-// Weights and x go through LDS, each wave's own piece, without a barrier: loads from
-// memory then take whole runs of a row.  With operands loaded in their own order
-// (16 bytes of x 64 bytes apart) 4 x 14336 x 4096 took 13.3 us instead of 8.3 (31 MB:
-// 3.8 TB/s), 16 x 4096 x 14336 18.5 instead of 11.9.
+// Weights and x go through LDS, each wave's own piece, without a barrier: neighbouring
+// lanes then load neighbouring pieces of a row.  With each lane loading its own row of
+// the operand, 4 x 14336 x 4096 took 12.4 us instead of 8.1 (31 MB: 3.9 TB/s),
+// 16 x 4096 x 14336 19.3 instead of 11.6 (32 MB, and 117 MB of x out of the L2s: the
+// loads of a CU take 10000 of its 25000 cycles, its LDS as many).
 #include "mx_device.hpp"
 #include "mx_layer.h"
 
@@ -30,7 +31,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Eight E2M1 codes (a dword) times the scale as a bf16 operand.
 __device__ __forceinline__ bf16x8 fp4_operand(uint32_t q, float scale) {
@@ -42,42 +43,8 @@ __device__ __forceinline__ bf16x8 fp4_operand(uint32_t q, float scale) {
   return u.v;
 }
 
-// x[k .. k + 7] of a token, +0 past K; rows of x need no alignment beyond their
-// type's.
-template <bool WHOLE>
-__device__ __forceinline__ uint4 load_x(const uint16_t* xrow, int64_t k, int64_t K) {
-  union { uint16_t h[8]; uint4 u; } r;
-  if (WHOLE || k + 8 <= K) {
-    __builtin_memcpy(&r.u, xrow + k, 16);
-  } else {
-    r.u = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int e = 0; e < 8; e++)
-      if (k + e < K) r.h[e] = xrow[k + e];
-  }
-  return r.u;
-}
-
-// x[k .. k + 7] of a token, +0 past K; rows of x need no alignment beyond their
-// type's.
-__device__ __forceinline__ uint4 load_x(const uint16_t* xrow, int64_t k, int64_t K) {
-  union { uint16_t h[8]; uint4 u; } r;
-  r.u = make_uint4(0, 0, 0, 0);
-  if (k + 8 <= K) __builtin_memcpy(&r.u, xrow + k, 16);
-  return r.u;
-}
-__device__ __forceinline__ void load_x_tail(const uint16_t* xrow, int64_t k, int64_t K, uint4& x) {
-  if (k >= K || k + 8 <= K) return;
-  union { uint16_t h[8]; uint4 u; } r;
-  r.u = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int e = 0; e < 8; e++)
-    if (k + e < K) r.h[e] = xrow[k + e];
-  x = r.u;
-}
-
-// One wave's piece of LDS, and what a lane loads for it in a step of 128 NI elements
-// of K.  All loads take whole runs of a row, 64 NI bytes of weights and 256 NI of x.
+// One wave's piece of LDS, which holds a step of 128 NI elements of K.  All loads take
+// whole runs of a row, 64 NI bytes of weights and 256 NI of x.
 template <int TOK, int NI, int R>
 struct Step {
   static constexpr int ROWS = 16 * R;
@@ -86,8 +53,6 @@ struct Step {
   static constexpr int BYTES = X_AT + TOK * X_PITCH;
   static constexpr int XL = (TOK * NI + 3) / 4;
   static constexpr int SCALED = 64 / (4 * NI);  // steps that one load of scales serves
-  uint4 q[R * NI];
-  uint4 x[XL];
 };
 
 struct Rows {
@@ -98,81 +63,108 @@ struct Rows {
   int nb, rows, live;  // rows and tokens that there are
 };
 
-// Blocks at or past `end` read as zeros; rows and tokens past the last as the last.
+// Rows and tokens past the last are the last.  Blocks at or past `end`, and pieces of x
+// that are not whole within K, take the first weights' bytes in their place: every
+// step then has the same number of loads, which is what lets a wait leave the later
+// steps' loads in flight.
 template <int TOK, int NI, int R>
-__device__ __forceinline__ void load_weights(Step<TOK, NI, R>& st, const Rows& w, int b0, int end) {
+__device__ __forceinline__ void load_weights(u32x4 (&q)[R * NI], const Rows& w, int b0, int end) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int r = 0; r < R * NI; r++) {
     const int f = 64 * r + lane, row = f / (4 * NI), b = b0 + f % (4 * NI);
-    st.q[r] = make_uint4(0, 0, 0, 0);
-    if (b < end) st.q[r] = *(const uint4*)(w.q + ((int64_t)(row < w.rows ? row : w.rows - 1) * w.nb + b) * 16);
+    const int64_t at = ((int64_t)(row < w.rows ? row : w.rows - 1) * w.nb + b) * 16;
+    q[r] = *(const u32x4*)(w.q + (b < end ? at : 0));
   }
 }
-template <int TOK, int NI, int R>
-__device__ __forceinline__ void load_tokens(Step<TOK, NI, R>& st, const Rows& w, int b0) {
+template <int TOK, int NI, int R, int XL>
+__device__ __forceinline__ void load_tokens(u32x4 (&x)[XL], const Rows& w, int b0, int end) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int r = 0; r < Step<TOK, NI, R>::XL; r++) {
+  for (int r = 0; r < XL; r++) {
     const int f = 64 * r + lane, tok = f / (16 * NI);
-    st.x[r] = load_x(w.x + (tok < w.live ? tok : w.live - 1) * w.ld_x, (int64_t)b0 * 32 + 8 * (f % (16 * NI)), w.K);
-  }
-  if ((w.K & 7) && (int64_t)(b0 + 4 * NI) * 32 > w.K) {
-#pragma unroll
-    for (int r = 0; r < Step<TOK, NI, R>::XL; r++) {
-      const int f = 64 * r + lane, tok = f / (16 * NI);
-      load_x_tail(w.x + (tok < w.live ? tok : w.live - 1) * w.ld_x, (int64_t)b0 * 32 + 8 * (f % (16 * NI)), w.K,
-                  st.x[r]);
-    }
+    const int64_t k = (int64_t)b0 * 32 + 8 * (f % (16 * NI));
+    const uint8_t* src = (const uint8_t*)(w.x + (tok < w.live ? tok : w.live - 1) * w.ld_x + k);
+    __builtin_memcpy(&x[r], b0 < end && k + 8 <= w.K ? src : w.q, 16);
   }
 }
-// scales of the 64 blocks from b0 on, four lanes a row
-template <int TOK, int NI, int R>
-__device__ __forceinline__ void load_scales(uint4 (&s)[R], const Rows& w, int b0) {
+// what load_tokens left out of a step that K ends in: the last elements, and zeros
+template <int TOK, int NI, int R, int XL>
+__device__ __forceinline__ void mend_tokens(u32x4 (&x)[XL], const Rows& w, int b0) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int r = 0; r < XL; r++) {
+    const int f = 64 * r + lane, tok = f / (16 * NI);
+    const int64_t k = (int64_t)b0 * 32 + 8 * (f % (16 * NI));
+    if (k + 8 <= w.K) continue;
+    const uint16_t* src = w.x + (tok < w.live ? tok : w.live - 1) * w.ld_x + k;
+    uint32_t h[8] = {};
+    if (k < w.K) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) h[e] = src[k + e < w.K ? e : 0];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) h[e] = k + e < w.K ? h[e] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) x[r][i] = h[2 * i] | h[2 * i + 1] << 16;
+  }
+}
+// Scales of the 64 blocks from b0 on, 16 blocks to each of four lanes a row.  Runs that
+// a row ends in are left to mend_scales.
+template <int R>
+__device__ __forceinline__ void load_scales(u32x4 (&s)[R], const Rows& w, int b0) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int a = 0; a < R; a++) {
     const int row = 16 * a + lane / 4, b = b0 + 16 * (lane & 3);
     const uint8_t* src = w.s + (int64_t)(row < w.rows ? row : w.rows - 1) * w.nb + b;
-    union { uint8_t c[16]; uint4 u; } t;
-    t.u = make_uint4(0, 0, 0, 0);
-    if (b + 16 <= w.nb) {
-      __builtin_memcpy(&t.u, src, 16);  // any alignment: rows of scales are nb bytes
-    } else {
+    __builtin_memcpy(&s[a], b + 16 <= w.nb ? src : w.q, 16);  // any alignment: rows of scales are nb bytes
+  }
+}
+template <int R>
+__device__ __forceinline__ void mend_scales(u32x4 (&s)[R], const Rows& w, int b0, int end) {
+  const int lane = threadIdx.x & 63, b = b0 + 16 * (lane & 3);
+  if (b >= end || b + 16 <= w.nb) return;  // runs past `end` are of no step
 #pragma unroll
-      for (int e = 0; e < 16; e++)
-        if (b + e < w.nb) t.c[e] = src[e];
-    }
-    s[a] = t.u;
+  for (int a = 0; a < R; a++) {
+    const int row = 16 * a + lane / 4;
+    const uint8_t* src = w.s + (int64_t)(row < w.rows ? row : w.rows - 1) * w.nb + b;
+    uint32_t c[16];
+#pragma unroll
+    for (int e = 0; e < 16; e++) c[e] = src[b + e < w.nb ? e : 0];
+#pragma unroll
+    for (int e = 0; e < 16; e++) c[e] = b + e < w.nb ? c[e] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) s[a][i] = c[4 * i] | c[4 * i + 1] << 8 | c[4 * i + 2] << 16 | c[4 * i + 3] << 24;
   }
 }
 template <int TOK, int NI, int R>
-__device__ __forceinline__ void stage_weights(const Step<TOK, NI, R>& st, uint8_t* lds) {
+__device__ __forceinline__ void stage_weights(const u32x4 (&q)[R * NI], uint8_t* lds) {
   using St = Step<TOK, NI, R>;
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int r = 0; r < R * NI; r++) {
     const int f = 64 * r + lane;
-    *(uint4*)(lds + St::Q_AT + f / (4 * NI) * St::Q_PITCH + f % (4 * NI) * 16) = st.q[r];
+    *(u32x4*)(lds + St::Q_AT + f / (4 * NI) * St::Q_PITCH + f % (4 * NI) * 16) = q[r];
   }
 }
-template <int TOK, int NI, int R>
-__device__ __forceinline__ void stage_tokens(const Step<TOK, NI, R>& st, uint8_t* lds) {
+template <int TOK, int NI, int R, int XL>
+__device__ __forceinline__ void stage_tokens(const u32x4 (&x)[XL], uint8_t* lds) {
   using St = Step<TOK, NI, R>;
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int r = 0; r < St::XL; r++) {
+  for (int r = 0; r < XL; r++) {
     const int f = 64 * r + lane;
     if (TOK * NI < 4 && f >= 16 * NI * TOK) break;  // fewer lanes hold a piece
-    *(uint4*)(lds + St::X_AT + f / (16 * NI) * St::X_PITCH + f % (16 * NI) * 16) = st.x[r];
+    *(u32x4*)(lds + St::X_AT + f / (16 * NI) * St::X_PITCH + f % (16 * NI) * 16) = x[r];
   }
 }
 template <int TOK, int NI, int R>
-__device__ __forceinline__ void stage_scales(const uint4 (&s)[R], uint8_t* lds) {
+__device__ __forceinline__ void stage_scales(const u32x4 (&s)[R], uint8_t* lds) {
   using St = Step<TOK, NI, R>;
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int a = 0; a < R; a++) *(uint4*)(lds + St::S_AT + (16 * a + lane / 4) * St::S_PITCH + 16 * (lane & 3)) = s[a];
+  for (int a = 0; a < R; a++) *(u32x4*)(lds + St::S_AT + (16 * a + lane / 4) * St::S_PITCH + 16 * (lane & 3)) = s[a];
 }
 // lanes of one wave: what one wrote to LDS, the others read
 __device__ __forceinline__ void wave_fence() {
@@ -216,11 +208,12 @@ __device__ __forceinline__ void take_step(const uint8_t* lds, int at, f32x4 (&ac
   }
 }
 
-// TOK tokens (1, 2, 4, 8, 16 or 32) and 16 R rows of W by one workgroup.
-template <int TOK, int NI, int WAVES, int R, bool BF16>
+// TOK tokens (1, 2, 4, 8, 16 or 32) and 16 R rows of W by one workgroup; weights D
+// steps ahead.
+template <int TOK, int NI, int WAVES, int R, int D, bool BF16>
 __global__ __launch_bounds__(64 * WAVES) void k_gemv(GemvArgs p) {
   using St = Step<TOK, NI, R>;
-  constexpr int MT = (TOK + 15) / 16, ROWS = 16 * R;
+  constexpr int MT = (TOK + 15) / 16, ROWS = 16 * R, XL = St::XL;
   constexpr int PART = 4 * MT * 16 * (ROWS + 1);  // bytes of a wave's partial sums
   __shared__ __align__(16) uint8_t lds[WAVES * (St::BYTES > PART ? St::BYTES : PART)];
   const int lane = threadIdx.x & 63, g = lane >> 4;
@@ -248,26 +241,40 @@ __global__ __launch_bounds__(64 * WAVES) void k_gemv(GemvArgs p) {
   const int end = s + per < steps ? s + per : steps;
   if (s < end) {
     const int last = end * STEP < w.nb ? end * STEP : w.nb;
-    St st;
-    uint4 sc[R];
-    load_scales<TOK, NI, R>(sc, w, s * STEP);
-    load_tokens<TOK, NI, R>(st, w, s * STEP);
-    load_weights<TOK, NI, R>(st, w, s * STEP, last);
+    u32x4 q[D][R * NI], x[XL], sc[R];
+    load_scales(sc, w, s * STEP);
+#pragma unroll
+    for (int d = 0; d < D; d++) {
+      if (d == 0) load_tokens<TOK, NI, R>(x, w, s * STEP, last);
+      load_weights<TOK, NI, R>(q[d], w, (s + d) * STEP, last);
+    }
+    mend_scales(sc, w, s * STEP, last);
     stage_scales<TOK, NI, R>(sc, mine);
-    for (int at = 0;;) {
-      stage_weights<TOK, NI, R>(st, mine);
-      stage_tokens<TOK, NI, R>(st, mine);
-      wave_fence();
-      s++;
-      if (s < end) {
-        load_tokens<TOK, NI, R>(st, w, s * STEP);
-        load_weights<TOK, NI, R>(st, w, s * STEP, last);
-        if (at == St::SCALED - 1) load_scales<TOK, NI, R>(sc, w, s * STEP);
+    // one exit, at the end of D steps: with one at each, a wait would have to cover
+    // the loads of whichever step came last
+    for (int at = 0; s < end;) {
+      const bool turn = at == St::SCALED - D;  // the D steps after these need other scales
+      if (turn) load_scales(sc, w, s + D < end ? (s + D) * STEP : w.nb);
+#pragma unroll
+      for (int d = 0; d < D; d++) {
+        const bool live = d == 0 || s < end;
+        if (live) {
+          if ((int64_t)(s + 1) * STEP * 32 > p.K) mend_tokens<TOK, NI, R>(x, w, s * STEP);
+          stage_weights<TOK, NI, R>(q[d], mine);
+          stage_tokens<TOK, NI, R>(x, mine);
+          wave_fence();
+        }
+        load_tokens<TOK, NI, R>(x, w, (s + 1) * STEP, last);
+        load_weights<TOK, NI, R>(q[d], w, (s + D) * STEP, last);
+        if (live) {
+          take_step<TOK, NI, R>(mine, at + d, acc);
+          wave_fence();
+        }
+        s++;
       }
-      take_step<TOK, NI, R>(mine, at, acc);
-      wave_fence();
-      if (s >= end) break;
-      if (++at == St::SCALED) {
+      at += D;
+      if (turn) {
+        mend_scales(sc, w, s * STEP, last);
         stage_scales<TOK, NI, R>(sc, mine);
         at = 0;
       }
@@ -296,11 +303,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_gemv(GemvArgs p) {
   }
 }
 
-template <int TOK, int NI, int WAVES, int R>
+template <int TOK, int NI, int WAVES, int R, int D>
 void go(const GemvArgs& a, hipStream_t st) {
   const dim3 g((unsigned)((a.N + 16 * R - 1) / (16 * R)), (unsigned)((a.M + TOK - 1) / TOK)), b(64 * WAVES);
-  if (a.bf16) hipLaunchKernelGGL((k_gemv<TOK, NI, WAVES, R, true>), g, b, 0, st, a);
-  else hipLaunchKernelGGL((k_gemv<TOK, NI, WAVES, R, false>), g, b, 0, st, a);
+  if (a.bf16) hipLaunchKernelGGL((k_gemv<TOK, NI, WAVES, R, D, true>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((k_gemv<TOK, NI, WAVES, R, D, false>), g, b, 0, st, a);
 }
 
 }  // namespace
@@ -312,14 +319,17 @@ void go(const GemvArgs& a, hipStream_t st) {
 //   1 x 4096 x 14336   7.9 / 10.6     1 x 14336 x 4096    8.1 / 7.7
 //   4 x 14336 x 4096   9.2 / 8.3      16 x 14336 x 4096  17.9 / 11.1 (two groups)
 //   16 x 4096 x 14336 11.9 / 19.3     32 x 14336 x 14336 71.0 / 45.0 (four groups)
+// Weights are loaded one step ahead, for 32 tokens, whose steps are half as wide, two
+// (one / two steps ahead, us): 32 x 4096 x 4096 7.6 / 7.3, 32 x 14336 x 14336 41.2 / 36.0,
+// but 4 x 14336 x 4096 8.1 / 9.1, 1 x 4096 x 14336 7.9 / 8.5, 16 x 4096 x 14336 11.9 / 12.4.
 hipError_t launch_gemv(const GemvArgs& a, hipStream_t st) {
   const bool many = (a.N + 15) / 16 > 512;
-  if (a.M == 1) many ? go<1, 2, 4, 1>(a, st) : go<1, 2, 8, 1>(a, st);
-  else if (a.M == 2) many ? go<2, 2, 4, 1>(a, st) : go<2, 2, 8, 1>(a, st);
-  else if (a.M <= 4) many ? go<4, 2, 4, 1>(a, st) : go<4, 2, 8, 1>(a, st);
-  else if (a.M <= 8) many ? go<8, 2, 4, 1>(a, st) : go<8, 2, 8, 1>(a, st);
-  else if (a.M <= 16) many ? go<16, 2, 4, 2>(a, st) : go<16, 2, 8, 1>(a, st);
-  else many ? go<32, 1, 4, 4>(a, st) : go<32, 1, 8, 1>(a, st);  // 32 tokens a reading of the weights
+  if (a.M == 1) many ? go<1, 2, 4, 1, 1>(a, st) : go<1, 2, 8, 1, 1>(a, st);
+  else if (a.M == 2) many ? go<2, 2, 4, 1, 1>(a, st) : go<2, 2, 8, 1, 1>(a, st);
+  else if (a.M <= 4) many ? go<4, 2, 4, 1, 1>(a, st) : go<4, 2, 8, 1, 1>(a, st);
+  else if (a.M <= 8) many ? go<8, 2, 4, 1, 1>(a, st) : go<8, 2, 8, 1, 1>(a, st);
+  else if (a.M <= 16) many ? go<16, 2, 4, 2, 1>(a, st) : go<16, 2, 8, 1, 1>(a, st);
+  else many ? go<32, 1, 4, 4, 2>(a, st) : go<32, 1, 8, 1, 2>(a, st);  // 32 tokens a reading of the weights
   return hipGetLastError();
 }
 

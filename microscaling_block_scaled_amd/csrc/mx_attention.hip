@@ -95,7 +95,7 @@ struct AttnArgs {
   int rows;              // Lq * group
   int splits;
   int chunk;             // tokens of a piece, a multiple of what its waves take at a time
-  uint32_t page16, magic;  // page / 16 and the constant that divides by it
+  uint32_t page16, magic, shift;  // page / 16 and the constants that divide by it
   // sums and (base, l) of the pieces: by rows [B][heads][rows][splits][dim] and [2], or
   // by tiles of 16 rows [B][heads][tiles][splits][dim / 16][64 lanes][4] and [16][2]
   float *part_o, *part_ml;
@@ -150,6 +150,13 @@ struct Stage {
   static constexpr int BYTES = VS_AT + 32 * SP;
 };
 
+// i / page16 for i < 2^27: with 2^(L - 1) < page16 <= 2^L, the constant c =
+// ceil(2^(27 + L) / page16) is too large by less than 1, so i c / 2^(27 + L) by less
+// than 1 / 2^L <= 1 / page16.  magic is 16 c, which has 32 bits, and shift L - 1.
+__device__ __forceinline__ uint32_t page_index(const AttnArgs& p, uint32_t i) {
+  return p.page16 == 1 ? i : __umulhi(i, p.magic) >> p.shift;
+}
+
 // The page of tokens t0 + 16 (l & 1) .. of a request in lane l, -1 where there are
 // none.  By a vector load and a step ahead of its use: a wave that waits for a page
 // number before it can load tokens does nothing else meanwhile.
@@ -157,7 +164,7 @@ __device__ __forceinline__ int page_of(const AttnArgs& p, const int32_t* table, 
   const int tok = t0 + 16 * (int)(threadIdx.x & 1);
   if (tok >= end) return -1;
   const uint32_t i16 = (uint32_t)tok >> 4;
-  return table[p.page16 == 1 ? i16 : __umulhi(i16, p.magic)];
+  return table[page_index(p, i16)];
 }
 // Row (page, head, place) of the cache at which tokens t0 + 16 u .. begin.  A page
 // that is not one of the cache's holds no tokens; any row stands in for it, and what
@@ -165,7 +172,7 @@ __device__ __forceinline__ int page_of(const AttnArgs& p, const int32_t* table, 
 __device__ __forceinline__ bool locate(const AttnArgs& p, int pages, int head, int t0, int u, int64_t& row) {
   const int pg = __builtin_amdgcn_readlane(pages, u);
   const uint32_t i16 = (uint32_t)(t0 + 16 * u) >> 4;
-  const uint32_t idx = p.page16 == 1 ? i16 : __umulhi(i16, p.magic);
+  const uint32_t idx = page_index(p, i16);
   const bool ok = (uint32_t)pg < (uint32_t)p.a.c.pages;
   row = ok ? ((int64_t)pg * p.a.c.heads + head) * p.a.c.page + (int)(i16 - idx * p.page16) * 16 : 0;
   return ok;
@@ -989,7 +996,11 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t st) {
   p.splits = r.splits;
   p.chunk = r.chunk;
   p.page16 = (uint32_t)a.c.page / 16;
-  p.magic = p.page16 > 1 ? (uint32_t)(((1ull << 32) + p.page16 - 1) / p.page16) : 0;
+  p.magic = p.shift = 0;
+  if (p.page16 > 1) {
+    while ((2u << p.shift) < p.page16) p.shift++;
+    p.magic = (uint32_t)(((1ull << (28 + p.shift)) + p.page16 - 1) / p.page16 << 4);
+  }
   p.part_o = a.work;
   const int64_t rows = r.shared ? (p.rows + 15) / 16 * 16 : p.rows;
   p.part_ml = a.work + (int64_t)a.B * a.c.heads * rows * r.splits * a.c.dim;

@@ -275,6 +275,40 @@ def test_past_4_gib(mx, oracle):
     assert torch.equal(big["k_q"][-1, :, -1], want["q_row"]) and torch.equal(big["v_s"][-1, :, -1], want["s_row"])
 
 
+@pytest.mark.parametrize("Lq", [1, 20])
+@pytest.mark.parametrize("page", [48, 65520])
+def test_pages_of_a_long_request(mx, page, Lq):
+    """26 million tokens, in pages whose size is no power of two: the page of every
+    token is found.  All but the last of a request's pages are one page of the cache; the
+    largest key is in the last 16 tokens of another, which the table names last."""
+    dim = 64
+    n = 400 * 65520 // page
+    cache = mx.kv_cache(3, 1, page, dim)
+    for t in cache.values():
+        t.zero_()
+    cache["k_s"].fill_(127)
+    cache["v_s"].fill_(127)
+    # page 0 holds ones, page 1 a key that every query takes, with fours; 2 is never named
+    cache["v_q"][0], cache["v_q"][1], cache["v_q"][2] = 0x38, 0x48, 0x7F
+    cache["k_q"][1, 0, page - 3] = 0x48  # 4: its score is 64 * 4 / 8 = 32 more than the others'
+    table = torch.zeros((1, n), dtype=torch.int32, device="cuda")
+    table[0, n - 1] = 1
+    q = torch.ones((1, Lq, 1, dim), dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([n * page], dtype=torch.int32, device="cuda")
+    say("attention over pages of a long request", page, Lq)
+    r = mx.attention(q, cache, mx.E4M3, table, lens)
+    got, lse = host(r["o"].float()).astype(np.float64), host(r["lse"]).astype(np.float64)
+    for i in range(Lq):
+        total = n * page - Lq + i + 1  # tokens that the query sees
+        fours = total - (n - 1) * page
+        top = np.exp(32.0) if total > n * page - 3 else 0.0
+        near = fours - (1 if top else 0)
+        l = (n - 1) * page + near + top
+        o = ((n - 1) * page + 4.0 * (near + top)) / l
+        assert np.abs(got[0, i] - o).max() <= 2.0 ** -7 * o, (i, got[0, i].max(), o)
+        assert abs(lse[0, i] - np.log(l)).max() <= 1e-4 * np.log(l), (i, lse[0, i], np.log(l))
+
+
 def test_other_stream_and_graph(mx, oracle):
     """On a stream that is handed over, and replayed from a graph, results are those of
     the eager call on the current stream."""

@@ -1,6 +1,6 @@
 /*
- * mx.h -- Microscaling (MX) block quantization and block-scaled matrix multiply
- * on AMD Instinct MI355X (gfx950).
+ * mx.h -- Microscaling (MX) block quantization, block-scaled matrix multiply and
+ * the decoder-layer operators around it on AMD Instinct MI355X (gfx950).
  *
  * Definitions followed ("Microscaling Data Formats for Deep Learning",
  * Rouhani et al., arXiv 2310.10537, source-linked summary page):
@@ -256,7 +256,8 @@ int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int32_t src);
  *   y       [M x N] fp32, leading dimension ld_y >= N.
  * A weight times its scale is exact in bf16 (for scale codes >= 1), so products are
  * exact and summed in fp32.  Made for M up to 32, where reading the weights is the
- * work: larger M is computed 32 tokens at a time, and mx_gemm is faster there.
+ * work: larger M (up to 32 * 65535) is computed 32 tokens at a time, and mx_gemm is
+ * faster there.  N up to 2^26, K < 2^31.
  */
 int mx_gemv(const void* x, int64_t ld_x, const void* w_q, const uint8_t* w_s, int32_t w_fmt, int64_t M, int64_t N,
             int64_t K, float* y, int64_t ld_y, mx_stream_t stream);
@@ -268,8 +269,9 @@ int mx_gemv_bf16(const void* x, int64_t ld_x, const void* w_q, const uint8_t* w_
  * A paged key/value cache in 8-bit MX.  Keys and values are each `pages` pages of
  * `page` tokens: elements [pages][heads][page][dim] in fmt, scales
  * [pages][heads][page][dim / 32].  A block is 32 consecutive values of one token's
- * head.  fmt MX_E4M3 or MX_E5M2; dim 64, 128 or 256; page a multiple of 16; all
- * four arrays 16-byte aligned (others: MX_ERR_UNSUPPORTED, MX_ERR_ALIGN).
+ * head.  fmt MX_E4M3 or MX_E5M2; dim 64, 128 or 256; page a multiple of 16 up to
+ * 65536, heads up to 65535; all four arrays 16-byte aligned (others:
+ * MX_ERR_UNSUPPORTED, MX_ERR_ALIGN).
  */
 typedef struct {
   void* k_q;
@@ -314,7 +316,8 @@ int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t h
  * A query that sees no token gets o = 0 and lse = -inf.  What the cache holds
  * beyond a query's tokens, NaN included, does not reach it.  Scores, sums and
  * outputs are held in fp32; the weights p are rounded to bf16 for the second
- * product.
+ * product.  B * heads and heads_q up to 65535, Lq * heads_q / heads up to 2^20 - 16,
+ * max_len up to 2^30 (more: MX_ERR_UNSUPPORTED).
  */
 int mx_attention(const mx_cache* cache, const void* q, int64_t ld_q, const int32_t* table, int64_t ld_table,
                  const int32_t* lens, int64_t B, int64_t Lq, int64_t heads_q, float scale, int64_t max_len,

@@ -28,7 +28,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // ---------------------------------------------------------------------------
 // A lane takes 8 elements of a token's head, keys and values (two loads in flight), a
 // quad one block.  Bound: HBM; at few tokens the launch.  Tokens of few elements
-// share a workgroup.
+// share a workgroup.  Measured, 8 heads of dim 128: 8192 tokens, 51 MB, 11.6 us
+// (4.4 TB/s; 15.5 with keys and values by different lanes and 64-bit indexes), 32
+// tokens 3.0.
 template <int SRC, int F>
 __device__ __forceinline__ void write_chunk(const uint32_t* raw, uint8_t* q, uint8_t* s, int c) {
   uint32_t v[8], am = 0, rnd[8];
@@ -47,7 +49,7 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift
   constexpr int ESZ = SRC == SRC_BF16 ? 2 : 4;
   const int per = p.c.heads << shift;  // chunks of a token's keys; 1 << shift of a head's
   const int sub = tokens_per_wg > 1 ? (int)threadIdx.x / per : 0;
-  const int64_t tok = (int64_t)blockIdx.x * tokens_per_wg + sub;
+  const int64_t tok = workgroup() * tokens_per_wg + sub;
   if (sub >= tokens_per_wg || tok >= p.tokens) return;
   const int64_t slot = p.slots[tok];  // the same for the lanes of a quad
   if (slot < 0 || slot >= p.c.pages * p.c.page) return;
@@ -84,7 +86,7 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift
 // Bound for a few rows: HBM, 2 (D + D / 32) bytes a token and head.  Each wave loads
 // its 32 tokens in whole 1 KB runs and reads them again from its own piece of LDS:
 // with loads in the operands' order (16 bytes of a token 32 bytes apart, scales byte
-// by byte) 32 requests to 16384 took 165 us, 136 us now (4.9 TB/s).  The next 32
+// by byte) 32 requests to 16384 took 165 us, 138 us now (661 MB: 4.8 TB/s).  The next 32
 // tokens are in flight meanwhile.
 struct u64x2 { uint2 lo, hi; };
 
@@ -525,8 +527,13 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
 //      (row_of), tokens in the order of the second product's lanes (8 g + 4 u + r for
 //      token 16 u + 4 g + r), and the four 16-byte pieces of a row exchanged by row, so
 //      that both the writes and the reads spread over the banks
-// Bound: matrix and softmax instructions of the waves and LDS reads (16 KB a wave and
-// step for D = 128) alike.
+// Bound: the instructions of two workgroups a CU.  A step of a wave (32 tokens, 32 rows,
+// D = 128) is 32 matrix instructions of 16 cycles, 16 exponentials of 16 and about 180
+// others of 4, 1500 cycles in all, and takes 1500 to 1700; a workgroup's first loads take
+// 6000 and its outputs 2500 besides.  4 requests of 64 query tokens to 4096, 8 heads and
+// 32 query heads: 28 us and 8.6 us for the join; two prompts of up to 2048: 127 us.
+// Tried without gain: all reads of a step ahead of their use, scores scaled in the
+// exponent's subtraction, the first tokens loaded before the request's length is known.
 template <int D>
 struct Shared {
   static constexpr int KP = 2 * D + 16, K_BYTES = 32 * KP, BYTES = K_BYTES + D * 64;
@@ -971,7 +978,7 @@ hipError_t attention_by_fmt(const AttnArgs& p, const Plan& r, hipStream_t st) {
 hipError_t launch_cache_write(const CacheWriteArgs& a, hipStream_t st) {
   const int shift = a.c.dim == 64 ? 3 : a.c.dim == 128 ? 4 : 5, per = a.c.heads << shift;
   const int tpw = per >= 256 ? 1 : 256 / per;
-  const dim3 g((unsigned)((a.tokens + tpw - 1) / tpw)), b(256);
+  const dim3 g = grid_of((a.tokens + tpw - 1) / tpw), b(256);
   if (a.src == SRC_BF16) {
     if (a.c.fmt == E4M3) hipLaunchKernelGGL((k_cache_write<SRC_BF16, E4M3>), g, b, 0, st, a, shift, tpw);
     else hipLaunchKernelGGL((k_cache_write<SRC_BF16, E5M2>), g, b, 0, st, a, shift, tpw);

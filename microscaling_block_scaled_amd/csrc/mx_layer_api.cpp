@@ -27,6 +27,7 @@ int check_rows(const void* p, int64_t ld, int64_t cols, int64_t esz) {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 constexpr int64_t kMaxNormCols = (int64_t)1 << 24;
+constexpr int64_t kMaxGemvRows = (int64_t)1 << 26;  // of W: 32 threads a row, fewer than 2^32 in a launch
 
 int check_cache(const mx_cache* c) {
   if (!c || !fmt_ok(c->fmt) || c->pages < 0 || c->heads < 0 || c->page <= 0 || c->dim <= 0) return MX_ERR_ARG;
@@ -64,7 +65,7 @@ int gemv(const void* x, int64_t ld_x, const void* w_q, const uint8_t* w_s, int32
   if (M == 0 || N == 0) return MX_OK;
   if (!y || (K > 0 && (!x || !w_q || !w_s))) return MX_ERR_ARG;
   if (!aligned(x, 2) || !aligned(w_q, 16) || !aligned(y, bf16 ? 2 : 4)) return MX_ERR_ALIGN;
-  if (M > (int64_t)32 * 65535 || N >= kMaxRows || K >= kMaxRows) return MX_ERR_UNSUPPORTED;
+  if (M > (int64_t)32 * 65535 || N > kMaxGemvRows || K >= kMaxRows) return MX_ERR_UNSUPPORTED;
   mx::GemvArgs a;
   a.x = (const uint16_t*)x;
   a.ld_x = ld_x;

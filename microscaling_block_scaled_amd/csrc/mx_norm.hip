@@ -11,12 +11,15 @@
 //   dx = rstd * (g - xhat * mean(g * xhat)) + dh      (dh: the gradient of h)
 //   dw = sum over rows of dy * xhat
 //
-// Bound: HBM.  A row is read once and stays in registers between the sum over
-// the row and the output.  A lane holds chunks of 8 consecutive elements, so
-// the four lanes of a quad hold one MX block and its maximum takes two DPP
-// exchanges.  Rows of many-row tensors that fit (up to 4096 elements) belong to
-// one wave each, which needs no barrier; wider rows, and tensors with too few
-// rows to fill the chip with waves, take the eight waves of a workgroup a row.
+// Bound: HBM; for a few rows the launch and the latency of two passes of a wave over
+// its registers.  A row is read once and stays in registers between the sum over the
+// row and the output.  A lane holds chunks of 8 consecutive elements, so the four lanes
+// of a quad hold one MX block and its maximum takes two DPP exchanges.  A row goes to
+// as many waves as give each lane one chunk (one for up to 512 elements, eight from
+// 2049 on), and to more chunks a lane only beyond 4096 elements.
+// Measured: 16384 x 4096 bf16 with a residual, 472 MB: 84.8 us (5.6 TB/s; a copy of
+// 1 GiB runs at 5.2); one row of 4096: 2.7 us.  The gradient of 8192 x 4096 with dh,
+// 268 MB: 45.9 us and 4.7 us for the sum of the partial sums.
 #include "mx_layer.h"
 #include "mx_rows.hpp"
 #include "mx_wave.hpp"
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(W < 8 ? 256 : WG) void k_norm_quant(NormArgs p) {
   __shared__ float red[8];
   const int t = (int)threadIdx.x & (T - 1);
   const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
-  const int64_t last = (int64_t)blockIdx.x * RPB + group;
+  const int64_t last = workgroup() * RPB + group;
   // past the last row: a row of no elements, for the barrier's sake
   const bool live = last < p.rows;
   const int64_t row = live ? last : 0;
@@ -214,7 +217,8 @@ template <int SRC, int F>
 __global__ __launch_bounds__(WG) void k_norm_quant_wide(NormArgs p) {
   constexpr int ESZ = SRC == SRC_BF16 ? 2 : 4;
   __shared__ float red[WG / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = workgroup();
+  if (row >= p.rows) return;
   const int cols = (int)p.cols, nch = (cols + 31) / 32 * 4;
   const uint8_t* x = (const uint8_t*)p.x + row * p.ld_x;
   const uint8_t* r = p.r ? (const uint8_t*)p.r + row * p.ld_r : nullptr;
@@ -466,11 +470,13 @@ constexpr int64_t kMaxCols = 16384;  // 8 waves x 64 lanes x 4 chunks of 8
 // the gradient kernel's row in registers: h, dy, dh, the next row's, w and dw
 constexpr int64_t grad_max_cols(int src) { return src == SRC_BF16 ? 16384 : 8192; }
 
+// Waves a row.  Measured (us; as here / half the waves with two chunks a lane / eight
+// waves): 16384 x 1024 22.9 / 23.7 / 38.1, 8192 x 2048 23.3 / 24.0 / 25.1,
+// 8192 x 4096 42.3 / 47.2 / 42.3; 16384 x 512 14.4 and by eight waves 35.0.
 template <int SRC, int F>
 hipError_t norm_launch(const NormArgs& a, hipStream_t st) {
-  const unsigned rows = (unsigned)a.rows;
   const dim3 b(a.cols <= 2048 ? 256 : WG);
-  auto grid = [&](unsigned per) { return dim3((rows + per - 1) / per); };
+  auto grid = [&](int per) { return grid_of((a.rows + per - 1) / per); };
   if (a.cols <= 512) hipLaunchKernelGGL((k_norm_quant<SRC, F, 1, 1>), grid(4), b, 0, st, a);
   else if (a.cols <= 1024) hipLaunchKernelGGL((k_norm_quant<SRC, F, 2, 1>), grid(2), b, 0, st, a);
   else if (a.cols <= 2048) hipLaunchKernelGGL((k_norm_quant<SRC, F, 4, 1>), grid(1), b, 0, st, a);
@@ -493,8 +499,10 @@ hipError_t norm_by_fmt(const NormArgs& a, hipStream_t st) {
   }
 }
 
-// Waves that share a row in the gradient kernel: a chunk a lane where eight
-// waves suffice.
+// Waves that share a row in the gradient kernel: a chunk a lane where eight waves
+// suffice.  Measured (us; as here / half the waves with two chunks / eight waves):
+// 16384 x 1024 24.1 / 24.4 / 53.1, 8192 x 2048 23.7 / 24.1 / 32.0,
+// 8192 x 4096 44.5 / 44.5 / 44.4.
 int grad_waves(int64_t cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : 8; }
 
 template <int SRC>
@@ -527,7 +535,9 @@ hipError_t launch_norm_quant(const NormArgs& a, hipStream_t st) {
   return a.src == SRC_BF16 ? norm_by_fmt<SRC_BF16>(a, st) : norm_by_fmt<SRC_F32>(a, st);
 }
 
-// Workgroups, and so rows of partial sums of dw.
+// Workgroups, and so rows of partial sums of dw: one a CU (8192 x 4096, both kernels:
+// 50.6 us with 256; with 128, 512 and 1024 it took longer, by the loads in flight or by
+// the partial sums).
 int64_t norm_grad_partials(int64_t rows, int64_t cols, int src) {
   if (cols > grad_max_cols(src)) return rows < 64 ? rows : 64;
   const int64_t per = (WG / 64) / grad_waves(cols), n = (rows + per - 1) / per;

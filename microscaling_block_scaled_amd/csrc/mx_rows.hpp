@@ -94,4 +94,12 @@ __device__ __forceinline__ void load_elems(const uint8_t* src, int valid, uint32
   }
 }
 
+// Launches of many workgroups: one dimension of a grid holds fewer than 2^32 threads.
+constexpr int GRID_BITS = 20;
+inline dim3 grid_of(int64_t workgroups) {
+  const int64_t most = (int64_t)1 << GRID_BITS;
+  return dim3((unsigned)(workgroups < most ? workgroups : most), (unsigned)((workgroups + most - 1) / most));
+}
+__device__ __forceinline__ int64_t workgroup() { return ((int64_t)blockIdx.y << GRID_BITS) + blockIdx.x; }
+
 }  // namespace mx

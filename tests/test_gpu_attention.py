@@ -76,6 +76,22 @@ def test_write_broadcast(mx):
     assert all(torch.equal(c[n], d[n]) for n in c)
 
 
+def test_write_of_more_tokens_than_a_grid_holds_threads_for(mx):
+    """2^24 tokens and some of 32 heads, a workgroup of 256 threads each; all but a few
+    have no slot."""
+    tokens = 2 ** 24 + 5
+    k, v = (torch.randn((1, 32, 64), device="cuda") for _ in range(2))
+    slots = torch.full((tokens,), -1, dtype=torch.int64, device="cuda")
+    slots[3], slots[-1] = 1, 17
+    c, d = mx.kv_cache(2, 32, 16, 64), mx.kv_cache(2, 32, 16, 64)
+    for t in (*c.values(), *d.values()):
+        t.zero_()
+    say("cache write of 2^24 tokens")
+    mx.cache_write(k.expand(tokens, 32, 64), v.expand(tokens, 32, 64), slots, c, mx.E4M3)
+    mx.cache_write(k.repeat(2, 1, 1), v.repeat(2, 1, 1), torch.tensor([1, 17], device="cuda"), d, mx.E4M3)
+    assert all(torch.equal(c[n], d[n]) for n in c)
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------

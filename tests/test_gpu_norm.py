@@ -206,6 +206,22 @@ def test_gradient_in_place_and_repeatable(mx):
             assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dw"], b["dw"]), which
 
 
+def test_more_rows_than_a_grid_holds_threads_for(mx):
+    """2^26 rows and some: workgroups of four rows, 256 threads each, pass 2^32 threads, and
+    offsets 32 bits.  The last rows are those of a call of their own."""
+    rows, n = 2 ** 26 + 11, 1003
+    x = torch.zeros((rows, 32), dtype=torch.bfloat16, device="cuda")
+    x[:n] = torch.randn((n, 32), device="cuda").bfloat16()
+    x[-n:] = torch.randn((n, 32), device="cuda").bfloat16()
+    w = torch.rand(32, device="cuda").bfloat16()
+    say("norm of 2^26 rows")
+    a = mx.rmsnorm_quantize(x, w, mx.E4M3)
+    for part in (slice(0, n), slice(rows - n, rows)):
+        b = mx.rmsnorm_quantize(x[part], w, mx.E4M3)
+        for name in ("q_row", "s_row", "rstd"):
+            assert torch.equal(a[name][part], b[name]), name
+
+
 def test_empty(mx):
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")
     o = mx.rmsnorm_quantize(e(0, 64), e(64), mx.E4M3)

@@ -233,14 +233,6 @@ def _empty(dtype, device, stream, *shape):
         return torch.empty(*shape, dtype=dtype, device=device)
 
 
-def _new_rows(rows, cols, dtype, device, stream):
-    """A new [rows, cols] tensor whose rows start on 16 bytes."""
-    per = 8 if dtype == torch.bfloat16 else 4
-    if cols % per == 0:
-        return _empty(dtype, device, stream, rows, cols)
-    return _empty(dtype, device, stream, rows, -(-cols // per) * per)[:, :cols]
-
-
 def _rows(t, shape, dtype, dev, what):
     """Checks a row-major matrix; its address and pitch.  The pitch of a single row
     says nothing: one that is allowed is given."""
@@ -257,6 +249,29 @@ def _flat(t, shape, dtype, dev, what):
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on device {dev}")
     return t.data_ptr()
+
+
+def _out(o, name, shape, dtype, dev, device, stream):
+    """The address of output `name`, a contiguous tensor: the caller's, or a new one."""
+    t = o.get(name)
+    if t is not None:
+        return _flat(t, shape, dtype, dev, name)
+    t = o[name] = _empty(dtype, device, stream, *shape)
+    return t.data_ptr()
+
+
+def _out_rows(o, name, shape, dtype, dev, device, stream):
+    """The address and pitch of output `name`, a row-major matrix: the caller's, or a new
+    one whose rows start on 16 bytes."""
+    t = o.get(name)
+    if t is not None:
+        return _rows(t, shape, dtype, dev, name)
+    rows, cols = shape
+    per = 8 if dtype == torch.bfloat16 else 4
+    pitch = -(-cols // per) * per
+    t = _empty(dtype, device, stream, rows, pitch)
+    o[name] = t if pitch == cols else t[:, :cols]
+    return t.data_ptr(), pitch
 
 
 def _work(t, dev):
@@ -286,22 +301,17 @@ def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, fmt: int, eps: float = 1e
     o = dict(out) if out else {}
     nblk = (cols + 31) // 32
     packed = nblk * 4 * BITS[fmt]
-    if "q_row" not in o:
-        o["q_row"] = _empty(torch.uint8, device, stream, rows, packed)
-    if "s_row" not in o:
-        o["s_row"] = _empty(torch.uint8, device, stream, rows, nblk)
-    if "rstd" not in o:
-        o["rstd"] = _empty(torch.float32, device, stream, rows)
-    if residual is not None and "h" not in o:
-        o["h"] = _new_rows(rows, cols, dtype, device, stream)
-    if want_y and "y" not in o:
-        o["y"] = _new_rows(rows, cols, dtype, device, stream)
-    ph, ld_h = _rows(o["h"], shape, dtype, dev, "h") if "h" in o else (None, 0)
-    py, ld_y = _rows(o["y"], shape, dtype, dev, "y") if "y" in o else (None, 0)
+    u8 = torch.uint8
+    pq = _out(o, "q_row", (rows, packed), u8, dev, device, stream)
+    ps = _out(o, "s_row", (rows, nblk), u8, dev, device, stream)
+    prstd = _out(o, "rstd", (rows,), torch.float32, dev, device, stream)
+    ph, ld_h = py, ld_y = None, 0
+    if residual is not None or o.get("h") is not None:
+        ph, ld_h = _out_rows(o, "h", shape, dtype, dev, device, stream)
+    if want_y or o.get("y") is not None:
+        py, ld_y = _out_rows(o, "y", shape, dtype, dev, device, stream)
     _check(lib.mx_rmsnorm_quantize(px, ld_x, pr, ld_r, pw, rows, cols, _SRC[dtype], fmt, eps, ph, ld_h, py, ld_y,
-                                   _flat(o["q_row"], (rows, packed), torch.uint8, dev, "q_row"),
-                                   _flat(o["s_row"], (rows, nblk), torch.uint8, dev, "s_row"),
-                                   _flat(o["rstd"], (rows,), torch.float32, dev, "rstd"), handle),
+                                   pq, ps, prstd, handle),
            "mx_rmsnorm_quantize")
     return o
 
@@ -323,19 +333,15 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: t
     ph, ld_h = _rows(h, shape, dtype, dev, "h")
     pdh, ld_dh = (None, 0) if dh is None else _rows(dh, shape, dtype, dev, "dh")
     o = dict(out) if out else {}
-    if "dx" not in o:
-        o["dx"] = _new_rows(rows, cols, dtype, device, stream)
-    if "dw" not in o:
-        o["dw"] = _empty(torch.float32, device, stream, cols)
+    pdx, ld_dx = _out_rows(o, "dx", shape, dtype, dev, device, stream)
+    pdw = _out(o, "dw", (cols,), torch.float32, dev, device, stream)
     if workspace is None:
         need = lib.mx_rmsnorm_backward_workspace(rows, cols, src)
         if need > 0:
             workspace = _empty(torch.uint8, device, stream, need)
-    pdx, ld_dx = _rows(o["dx"], shape, dtype, dev, "dx")
     _check(lib.mx_rmsnorm_backward(pdy, ld_dy, ph, ld_h, _flat(w, (cols,), dtype, dev, "w"),
                                    _flat(rstd, (rows,), torch.float32, dev, "rstd"), pdh, ld_dh, rows, cols, src,
-                                   pdx, ld_dx, _flat(o["dw"], (cols,), torch.float32, dev, "dw"),
-                                   *_work(workspace, dev), handle), "mx_rmsnorm_backward")
+                                   pdx, ld_dx, pdw, *_work(workspace, dev), handle), "mx_rmsnorm_backward")
     return o
 
 
@@ -439,19 +445,18 @@ def attention(q: torch.Tensor, cache: dict, fmt: int, table: torch.Tensor, lens:
     per = table.shape[1]
     if max_len is None:
         max_len = per * c.page
+    elif max_len > per * c.page:  # whatever the distance of the table's rows is
+        raise MXError(MX_ERR_SHAPE, "mx_attention")
     o = dict(out) if out else {}
-    if "o" not in o:
-        o["o"] = _empty(torch.bfloat16, q.device, stream, B, Lq, heads_q, dim)
-    if "lse" not in o:
-        o["lse"] = _empty(torch.float32, q.device, stream, B, Lq, heads_q)
+    device = q.device
+    po = _out(o, "o", shape, torch.bfloat16, dev, device, stream)
+    plse = _out(o, "lse", (B, Lq, heads_q), torch.float32, dev, device, stream)
     if workspace is None:
         need = lib.mx_attention_workspace(B, Lq, heads_q, c.heads, dim, max_len)
         if need > 0:
-            workspace = _empty(torch.uint8, q.device, stream, need)
+            workspace = _empty(torch.uint8, device, stream, need)
     _check(lib.mx_attention(c, q.data_ptr(), ld_q, table.data_ptr(), table.stride(0) if B > 1 else per,
                             _flat(lens, (B,), torch.int32, dev, "lens"), B, Lq, heads_q,
                             dim ** -0.5 if scale is None else scale, max_len,
-                            _flat(o["o"], shape, torch.bfloat16, dev, "o"), heads_q * dim,
-                            _flat(o["lse"], (B, Lq, heads_q), torch.float32, dev, "lse"), *_work(workspace, dev), handle),
-           "mx_attention")
+                            po, heads_q * dim, plse, *_work(workspace, dev), handle), "mx_attention")
     return o

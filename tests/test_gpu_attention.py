@@ -415,3 +415,17 @@ def test_empty(mx):
         o = mx.attention(z(2, 1, 4, 64), cc, mx.E4M3, tab, lens)
         assert (o["o"] == 0).all() and torch.isneginf(o["lse"]).all()
     mx.cache_write(z(0, 2, 64), z(0, 2, 64), z(0, t=torch.int64), c, mx.E4M3)
+
+
+def test_bound_past_a_table_that_is_a_slice(mx):
+    """A table of 2 columns within rows of 8: a bound of 33 tokens in pages of 16 is refused."""
+    c = mx.kv_cache(4, 2, 16, 64)
+    wide = torch.zeros((2, 8), dtype=torch.int32, device="cuda")
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    lens = torch.full((2,), 20, dtype=torch.int32, device="cuda")
+    a = mx.attention(q, c, mx.E4M3, wide[:, :2], lens, max_len=32)
+    b = mx.attention(q, c, mx.E4M3, wide[:, :2].contiguous(), lens)
+    assert torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
+    with pytest.raises(mx.MXError) as err:
+        mx.attention(q, c, mx.E4M3, wide[:, :2], lens, max_len=33)
+    assert err.value.status == mx.MX_ERR_SHAPE

@@ -802,6 +802,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(AttnArgs p) {
   }
 }
 
+constexpr int MAX_PIECES = 16;  // of a request's tokens, where rows share them
+
 // Joins the pieces of 16 rows; each wave a quarter of their dims.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_join_rows(AttnArgs p) {
@@ -824,25 +826,53 @@ __global__ __launch_bounds__(256) void k_attention_join_rows(AttnArgs p) {
   const int mine = pieces(row0 + i), most = pieces(row0 + 15);
   const float* ml = p.part_ml + at * p.splits * 32 + 2 * i;
   const float* po = p.part_o + (at * p.splits * (D / 16) + wave * ND) * 256 + 4 * lane;
-  float m = -__builtin_inff(), l = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < mine; s++) m = __builtin_fmaxf(m, ml[32 * s]);
-  const float base = m == -__builtin_inff() ? 0.0f : m;
+  // sums AT pieces at a time, the next ones and all bases in flight meanwhile
+  constexpr int AT = D == 256 ? 2 : 4;
+  f32x4 next[AT][ND];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int k = 0; k < AT; k++)
+#pragma unroll
+      for (int d = 0; d < ND; d++) {
+        const int s = s0 + k < most ? s0 + k : most - 1;
+        next[k][d] = *(const f32x4*)(po + ((int64_t)s * (D / 16) + d) * 256);
+      }
+  };
   f32x4 o[ND];
 #pragma unroll
   for (int d = 0; d < ND; d++) o[d] = f32x4{0, 0, 0, 0};
-#pragma unroll 4
-  for (int s = 0; s < most; s++) {
-    f32x4 part[ND];
+  float m = -__builtin_inff(), l = 0.0f;
+  if (most > 0) {
+    f32x2 w[MAX_PIECES];
 #pragma unroll
-    for (int d = 0; d < ND; d++) part[d] = *(const f32x4*)(po + ((int64_t)s * (D / 16) + d) * 256);
-    const f32x2 w = s < mine ? *(const f32x2*)(ml + 32 * s) : f32x2{-__builtin_inff(), 0.0f};
-    const float a = __builtin_amdgcn_exp2f(w.x - base);
-    l += w.y * a;
+    for (int s = 0; s < MAX_PIECES; s++) {
+      w[s] = f32x2{-__builtin_inff(), 0.0f};
+      if (s < mine) w[s] = *(const f32x2*)(ml + 32 * s);
+    }
+    load(0);
 #pragma unroll
-    for (int d = 0; d < ND; d++)
+    for (int s = 0; s < MAX_PIECES; s++) m = __builtin_fmaxf(m, w[s].x);
+    const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
-      for (int e = 0; e < 4; e++) o[d][e] = s < mine ? __builtin_fmaf(part[d][e], a, o[d][e]) : o[d][e];
+    for (int s0 = 0; s0 < MAX_PIECES; s0 += AT) {
+      if (s0 >= most) break;
+      f32x4 part[AT][ND];
+#pragma unroll
+      for (int k = 0; k < AT; k++)
+#pragma unroll
+        for (int d = 0; d < ND; d++) part[k][d] = next[k][d];
+      if (s0 + AT < most) load(s0 + AT);
+#pragma unroll
+      for (int k = 0; k < AT; k++) {
+        const float a = __builtin_amdgcn_exp2f(w[s0 + k].x - base);
+        l += w[s0 + k].y * a;
+#pragma unroll
+        for (int d = 0; d < ND; d++)
+#pragma unroll
+          for (int e = 0; e < 4; e++)  // pieces that the row has no tokens in need not be numbers
+            o[d][e] = s0 + k < mine ? __builtin_fmaf(part[k][d][e], a, o[d][e]) : o[d][e];
+      }
+    }
   }
   put_rows<D, ND>(o, wave * ND, l, os);
   __syncthreads();
@@ -930,7 +960,7 @@ Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_l
   const int64_t units = (max_len + unit - 1) / unit;
   int64_t splits = r.waves == 8 ? 1 : ((!r.shared && dim == 256 ? 512 : 1024) + base - 1) / base;
   if (splits > (units + 1) / 2) splits = (units + 1) / 2;  // at least two steps a wave
-  if (r.shared && splits > 16) splits = 16;                // joining them costs a row's outputs each
+  if (r.shared && splits > MAX_PIECES) splits = MAX_PIECES;  // joining them costs a row's outputs each
   if (splits < 1) splits = 1;
   int64_t per = (units + splits - 1) / splits;
   if (per < 1) per = 1;

@@ -531,7 +531,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
 // D = 128) is 32 matrix instructions of 16 cycles, 16 exponentials of 16 and about 180
 // others of 4, 1500 cycles in all, and takes 1500 to 1700; a workgroup's first loads take
 // 6000 and its outputs 2500 besides.  4 requests of 64 query tokens to 4096, 8 heads and
-// 32 query heads: 28 us and 8.6 us for the join; two prompts of up to 2048: 127 us.
+// 32 query heads: 28 us and 7.2 us for the join; two prompts of up to 2048: 127 us.
 // Tried without gain: all reads of a step ahead of their use, scores scaled in the
 // exponent's subtraction, the first tokens loaded before the request's length is known.
 template <int D>
@@ -947,16 +947,22 @@ struct Plan {
 // 22.1 by rows, 32 rows 29.4 and 24.0, 64 rows 35 and 27).  Workgroups are wanted
 // twice for each that the chip holds at a time (two of four waves a CU, one for dim
 // 256), which evens out requests of different lengths: 32 requests to 16384, dim 128,
-// took 136 us in 4 pieces, 143 in 16.  Up to 1024 tokens of few rows eight waves of
-// one workgroup spare the second launch.
+// took 136 us in 4 pieces, 143 in 16.  Few rows of up to 1024 tokens go to eight waves of
+// one workgroup, without pieces and a second launch, and so do more tokens where
+// requests and heads fill the chip by themselves.  Measured, 8 heads of dim 128 (us;
+// eight waves / pieces and their join): 1 request of 1000 10.6 / 10.0 and a launch
+// more, of 2048 16.3 / 10.0; 8 to 2048 17.1 / 13.0; 16 to 2048 17.1 / 20.2, to 4096
+// 28.4 / 28.1; 32 to 2048 19.6 / 27.6, to 8192 69 / 78, to 16384 135 / 142, but there
+// one long request among short ones would take twice as long.
 Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_len) {
   Plan r;
   const int64_t rows = Lq * group;
   r.shared = rows > 16;
   r.nr = rows > 64 && dim < 256 ? 2 : 1;
-  r.waves = !r.shared && dim < 256 && max_len <= 1024 ? 8 : 4;
   r.tiles = r.shared ? (int)((rows + 64 * r.nr - 1) / (64 * r.nr)) : 1;
-  const int64_t unit = r.shared ? 128 : STEP * r.waves, base = B * heads * r.tiles;
+  const int64_t base = B * heads * r.tiles;
+  r.waves = !r.shared && dim < 256 && max_len <= (base >= 256 ? 8192 : base >= 128 ? 2048 : 1024) ? 8 : 4;
+  const int64_t unit = r.shared ? 128 : STEP * r.waves;
   const int64_t units = (max_len + unit - 1) / unit;
   int64_t splits = r.waves == 8 ? 1 : ((!r.shared && dim == 256 ? 512 : 1024) + base - 1) / base;
   if (splits > (units + 1) / 2) splits = (units + 1) / 2;  // at least two steps a wave

@@ -429,3 +429,13 @@ def test_bound_past_a_table_that_is_a_slice(mx):
     with pytest.raises(mx.MXError) as err:
         mx.attention(q, c, mx.E4M3, wide[:, :2], lens, max_len=33)
     assert err.value.status == mx.MX_ERR_SHAPE
+
+
+@pytest.mark.parametrize("B,most", [(16, 1100), (32, 2100)])
+def test_many_requests_without_pieces(mx, oracle, B, most):
+    """Requests and heads that fill the chip: more than 1024 tokens by one workgroup."""
+    rng = np.random.default_rng(B)
+    lens = [most, 0, 1] + [int(n) for n in rng.integers(1, 80, B - 3)]
+    c = Case(oracle, rng, lens, 1, 8, 2, 64, 16, 0)
+    say("attention, many requests", B, most)
+    c.compare(mx.attention(c.device(), c.dcache, 0, c.dtable, c.dlens), 64 ** -0.5)

@@ -6,6 +6,14 @@
       Meant to run under `rocprofv3 --kernel-trace` (R >= 100: per-dispatch
       medians) and under `rocprofv3 --pmc ...` (a few R per counter pass).
 
+  python -m microscaling_block_scaled_amd.profile_kernels layers [--reps R]
+      Runs each listed case of perf/operators.py (the decoder-layer operators)
+      R times, on three states by turns.
+
+  python -m microscaling_block_scaled_amd.profile_kernels launches TRACE_DIR [COUNTER_DIR ...]
+      A table of the kernels of such a run in launch order, by kernel and grid:
+      median duration and the medians of what the counter runs collected.
+
   python -m microscaling_block_scaled_amd.profile_kernels traffic FETCH_DIR WRITE_DIR OUT.json
       Reads the two counter runs (rocprofv3 --output-format csv), scales each
       kernel's per-dispatch FETCH_SIZE / WRITE_SIZE by what the counters read
@@ -181,6 +189,50 @@ def traffic(fetch_dir: str, write_dir: str, out: str) -> None:
     print(json.dumps(res, indent=1))
 
 
+def layers(reps: int) -> None:
+    import importlib.util
+
+    import torch
+
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    for case in ops.listed():
+        states = [ops.prepare(case, seed) for seed in range(3)]
+        torch.cuda.synchronize()
+        print(case["name"], flush=True)
+        for i in range(reps):
+            ops.run(states[i % 3])
+        torch.cuda.synchronize()
+
+
+def launches(trace_dir: str, counter_dirs: list) -> None:
+    """Grids tell the cases of one kernel apart."""
+    def name(r):
+        return r["Kernel_Name"].replace("(anonymous namespace)::", "").replace("void ", "").replace("mx::", "").split("(")[0]
+
+    rows = [r for r in _rows(trace_dir, "*kernel_trace.csv") if "mx::" in r["Kernel_Name"]]
+    dur: dict[tuple, list[float]] = {}
+    for r in sorted(rows, key=lambda r: int(r["Start_Timestamp"])):
+        threads = int(r["Grid_Size_X"]) * int(r["Grid_Size_Y"]) * int(r["Grid_Size_Z"])
+        dur.setdefault((name(r), threads), []).append(
+            (int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3)
+    got: dict[tuple, dict] = {}
+    for d in counter_dirs:
+        for r in _rows(d, "*counter_collection.csv"):
+            if "mx::" in r["Kernel_Name"]:
+                per = got.setdefault((name(r), int(r["Grid_Size"])), {})
+                per.setdefault(r["Counter_Name"], []).append(float(r["Counter_Value"]))
+    counters = sorted({c for per in got.values() for c in per})
+    print("| kernel | threads | launches | us |" + "".join(f" {c} |" for c in counters))
+    print("|---|---|---|---|" + "---|" * len(counters))
+    for key, t in dur.items():
+        per = got.get(key, {})
+        cells = "".join(f" {_median(per[c]):.0f} |" if c in per else " |" for c in counters)
+        print(f"| `{key[0]}` | {key[1]} | {len(t)} | {_median(t):.1f} |{cells}")
+
+
 def _durations(trace_dir: str) -> dict:
     """kernel name -> per-dispatch durations (us) in dispatch order."""
     out: dict[str, list[float]] = {}
@@ -300,6 +352,10 @@ def main(argv):
     if len(argv) >= 1 and argv[0] == "run":
         reps = int(argv[argv.index("--reps") + 1]) if "--reps" in argv else 3
         run(reps)
+    elif len(argv) >= 1 and argv[0] == "layers":
+        layers(int(argv[argv.index("--reps") + 1]) if "--reps" in argv else 12)
+    elif len(argv) >= 2 and argv[0] == "launches":
+        launches(argv[1], argv[2:])
     elif len(argv) == 4 and argv[0] == "traffic":
         traffic(argv[1], argv[2], argv[3])
     elif len(argv) == 4 and argv[0] == "stats":

@@ -315,8 +315,8 @@ int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t h
  *           use until the call's work is done.  MX_ERR_SHAPE if smaller.
  * A query that sees no token gets o = 0 and lse = -inf.  What the cache holds
  * beyond a query's tokens, NaN included, does not reach it.  Scores, sums and
- * outputs are held in fp32; the weights p are rounded to bf16 for the second
- * product.  B * heads and heads_q up to 65535, Lq * heads_q / heads up to 2^20 - 16,
+ * outputs are held in fp32; for the second product a weight is two bf16 terms, which
+ * keep it to 2^-15.  B * heads and heads_q up to 65535, Lq * heads_q / heads up to 2^20 - 16,
  * max_len up to 2^30 (more: MX_ERR_UNSUPPORTED).
  */
 int mx_attention(const mx_cache* cache, const void* q, int64_t ld_q, const int32_t* table, int64_t ld_table,

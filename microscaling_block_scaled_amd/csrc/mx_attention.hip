@@ -79,17 +79,15 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift
 //   O^T = V^T P^T those 8 scores (two groups of 16 tokens) are the lane's 8 of the
 //                 32 of a sum over tokens as they are; the lane takes dims
 //                 (l % 16) D/16 .. of the same 8 tokens and transposes 2 x 2
-// so P stays in registers.  P is rounded to bf16 (up to 2^-8 of itself, like the
-// output's own rounding; its sum l is of the unrounded p); scores, maxima, sums and O
-// stay in fp32.
+// so P stays in registers, as two bf16 terms (see `weights`); scores, maxima, sums and
+// O stay in fp32.
 //
 // Bound for a few rows: HBM, 2 (D + D / 32) bytes a token and head.  Each wave loads
 // its 32 tokens in whole 1 KB runs and reads them again from its own piece of LDS:
 // with loads in the operands' order (16 bytes of a token 32 bytes apart, scales byte
-// by byte) 32 requests to 16384 took 165 us, 138 us now (661 MB: 4.8 TB/s).  The next 32
+// by byte) 32 requests to 16384 took 165 us, 136 us this way, and 140 us with weights of
+// two terms (661 MB: 4.7 TB/s).  The next 32
 // tokens are in flight meanwhile.
-struct u64x2 { uint2 lo, hi; };
-
 constexpr int STEP = 32;  // tokens a wave takes at a time
 
 struct AttnArgs {
@@ -298,13 +296,36 @@ struct Sums {
   float m[NR], l[NR];   // l over the lane's tokens only
 };
 
-// Maxima, weights and sums of a step's scores (in units of log 2, masked); p as the
-// operand of the second product.  The base that scores are taken from is a maximum of
+// Weights of a step as operands of the second product: p is the sum of two bf16 terms.
+// hi is p cut to 8 bits; lo is what is left of it, and 2^-20 p, rounded: p is kept to
+// 2^-15 (one rounded term would leave 2^-8 of each weight, as much as the output's own
+// rounding).  lo is above zero where p is, so an infinite value stays one.  Measured (us,
+// one rounded term / these two): 32 requests to 16384 136 / 140, 1 of 1000 10.9 / 11.3;
+// where rows share tokens, 4 requests of 64 query tokens to 4096 27.2 / 28.7, two
+// prompts of 2048 128 / 147, by the second products and 24 more instructions for 8 weights.
+struct Weights {
+  bf16x8 hi, lo;
+};
+__device__ __forceinline__ Weights weights(const f32x4 (&p)[2]) {
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const float v0 = p[k >> 1][2 * (k & 1)], v1 = p[k >> 1][2 * (k & 1) + 1];
+    const uint32_t u0 = __builtin_bit_cast(uint32_t, v0), u1 = __builtin_bit_cast(uint32_t, v1);
+    hi[k] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
+    lo[k] = bf16_pair(__builtin_fmaf(v0, 1.0f + 0x1p-20f, -__builtin_bit_cast(float, u0 & 0xFFFF0000u)),
+                      __builtin_fmaf(v1, 1.0f + 0x1p-20f, -__builtin_bit_cast(float, u1 & 0xFFFF0000u)));
+  }
+  return {operand(hi[0], hi[1], hi[2], hi[3]), operand(lo[0], lo[1], lo[2], lo[3])};
+}
+
+// Maxima, weights and sums of a step's scores (in units of log 2, masked); the weights
+// p take the scores' place.  The base that scores are taken from is a maximum of
 // earlier ones: it moves, and the sums with it, only where a score passes it by more
 // than 8, so p stays below 2^8 and O is seldom multiplied.  o / l does not depend on
 // the base.
 template <int D, int NR>
-__device__ __forceinline__ void soften(f32x4 (&s)[NR][2], Sums<D, NR>& sum, bf16x8 (&pr)[NR]) {
+__device__ __forceinline__ void soften(f32x4 (&s)[NR][2], Sums<D, NR>& sum) {
 #pragma unroll
   for (int n = 0; n < NR; n++) {
     float v[8], top = -__builtin_inff();
@@ -327,8 +348,8 @@ __device__ __forceinline__ void soften(f32x4 (&s)[NR][2], Sums<D, NR>& sum, bf16
     for (int e = 0; e < 8; e++) {
       v[e] = __builtin_amdgcn_exp2f(v[e] - base);
       sum.l[n] += v[e];
+      s[n][e >> 2][e & 3] = v[e];
     }
-    pr[n] = operand(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
   }
 }
 
@@ -374,19 +395,19 @@ __device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[64], f
       s[0][e >> 2][e & 3] = seen ? s[0][e >> 2][e & 3] : -__builtin_inff();
     }
   }
-  bf16x8 pr[1];
-  soften<D, 1>(s, sum, pr);
+  soften<D, 1>(s, sum);
   if (odd) {
     // 0 * NaN is not 0: token by token, for the rows that see it.  p takes the
     // place of the keys.
     wave_fence();
-    uint16_t* ps = (uint16_t*)(lds + St::K_AT);  // [row][token]
-    *(uint2*)(ps + 32 * i + 4 * g) = __builtin_bit_cast(u64x2, pr[0]).lo;
-    *(uint2*)(ps + 32 * i + 16 + 4 * g) = __builtin_bit_cast(u64x2, pr[0]).hi;
+    float* ps = (float*)(lds + St::K_AT);  // [row][token]
+    static_assert(32 * St::KP >= 16 * STEP * 4, "weights fit into the keys' place");
+    *(f32x4*)(ps + STEP * i + 4 * g) = s[0][0];
+    *(f32x4*)(ps + STEP * i + 16 + 4 * g) = s[0][1];
     wave_fence();
     for (int tok = 0; tok < STEP; tok++) {
       if (tok >= limit) continue;
-      const float pt = __builtin_bit_cast(float, (uint32_t)ps[32 * i + tok] << 16);
+      const float pt = ps[STEP * i + tok];
 #pragma unroll
       for (int e = 0; e < 4; e++)
 #pragma unroll
@@ -405,15 +426,18 @@ __device__ __forceinline__ void take_step(uint8_t* lds, const bf16x8 (*q)[64], f
     }
     return;
   }
+  const Weights pr = weights(s[0]);
 #pragma unroll
   for (int k = 0; k < D / 64; k++) {
     uint32_t w[4][4];
     v_operands<D, F>(lds, k, w);
 #pragma unroll
-    for (int d = 0; d < 4; d++) {
-      const bf16x8 v = operand(w[d][0], w[d][1], w[d][2], w[d][3]);
-      sum.o[0][4 * k + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[0], sum.o[0][4 * k + d], 0, 0, 0);
-    }
+    for (int e = 0; e < 2; e++)
+#pragma unroll
+      for (int d = 0; d < 4; d++) {
+        const bf16x8 v = operand(w[d][0], w[d][1], w[d][2], w[d][3]);
+        sum.o[0][4 * k + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, e ? pr.lo : pr.hi, sum.o[0][4 * k + d], 0, 0, 0);
+      }
   }
 }
 
@@ -531,7 +555,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
 // D = 128) is 32 matrix instructions of 16 cycles, 16 exponentials of 16 and about 180
 // others of 4, 1500 cycles in all, and takes 1500 to 1700; a workgroup's first loads take
 // 6000 and its outputs 2500 besides.  4 requests of 64 query tokens to 4096, 8 heads and
-// 32 query heads: 28 us and 7.2 us for the join; two prompts of up to 2048: 127 us.
+// 32 query heads: 29 us and 7.1 us for the join; two prompts of up to 2048: 147 us.
 // Tried without gain: all reads of a step ahead of their use, scores scaled in the
 // exponent's subtraction, the first tokens loaded before the request's length is known.
 template <int D>
@@ -664,7 +688,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(AttnArgs p) {
   constexpr int OS = 16 * (D + 2) * 2;  // bytes of a wave's 16 rows of outputs
   static_assert(2 * Sh::BYTES >= 4 * OS, "outputs fit into the buffers");
   __shared__ __align__(16) uint8_t lds[2 * Sh::BYTES];
-  __shared__ __align__(16) uint16_t ps[4][16][32];
+  __shared__ __align__(16) float ps[4][16][STEP];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x, head = blockIdx.y % p.a.c.heads, b = blockIdx.y / p.a.c.heads;
@@ -747,19 +771,18 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(AttnArgs p) {
           s[n][e >> 2][e & 3] = seen ? s[n][e >> 2][e & 3] : -__builtin_inff();
         }
     }
-    bf16x8 pr[NR];
-    soften<D, NR>(s, sum, pr);
+    soften<D, NR>(s, sum);
     if (odd && p.a.Lq > 1) {
       // 0 * NaN is not 0: token by token, for the rows that see it
 #pragma unroll
       for (int n = 0; n < NR; n++) {
         wave_fence();
-        *(uint2*)&ps[wave][i][4 * g] = __builtin_bit_cast(u64x2, pr[n]).lo;
-        *(uint2*)&ps[wave][i][16 + 4 * g] = __builtin_bit_cast(u64x2, pr[n]).hi;
+        *(f32x4*)&ps[wave][i][4 * g] = s[n][0];
+        *(f32x4*)&ps[wave][i][16 + 4 * g] = s[n][1];
         wave_fence();
         for (int tok = 0; tok < STEP; tok++) {
           if (tok >= lim[n] - t) continue;
-          const float pt = __builtin_bit_cast(float, (uint32_t)ps[wave][i][tok] << 16);
+          const float pt = ps[wave][i][tok];
 #pragma unroll
           for (int d = 0; d < D / 16; d++)
 #pragma unroll
@@ -772,12 +795,22 @@ __global__ __launch_bounds__(256, 2) void k_attention_rows(AttnArgs p) {
       }
       continue;
     }
+    Weights pr[NR];
 #pragma unroll
-    for (int d = 0; d < D / 16; d++) {
-      const bf16x8 v = *(const bf16x8*)(buf + Sh::v_at(16 * d + i, g));
+    for (int n = 0; n < NR; n++) pr[n] = weights(s[n]);
 #pragma unroll
-      for (int n = 0; n < NR; n++)
-        sum.o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pr[n], sum.o[n][d], 0, 0, 0);
+    for (int d0 = 0; d0 < D / 16; d0 += 4) {
+      bf16x8 v[4];
+#pragma unroll
+      for (int d = 0; d < 4; d++) v[d] = *(const bf16x8*)(buf + Sh::v_at(16 * (d0 + d) + i, g));
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+#pragma unroll
+        for (int d = 0; d < 4; d++)
+#pragma unroll
+          for (int n = 0; n < NR; n++)
+            sum.o[n][d0 + d] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[d], e ? pr[n].lo : pr[n].hi, sum.o[n][d0 + d], 0, 0, 0);
     }
   }
   __syncthreads();  // the buffers hold outputs now

@@ -219,7 +219,8 @@ int mx_gemm_mx(const void* a_q, const uint8_t* a_s, int32_t a_fmt, const void* b
  *   rstd    [rows] fp32, for mx_rmsnorm_backward; NULL: not written.
  * Pointers to rows, w and q_row 16-byte aligned, leading dimensions multiples of
  * 16 bytes.  Any rows < 2^31 and cols <= 2^24.  A row whose mean square is not
- * finite gives what the formulas give.
+ * finite gives what the formulas give.  rows == 0 or cols == 0 writes nothing, rstd
+ * (0 / 0 for a row of no columns) included.
  */
 int mx_rmsnorm_quantize(const void* x, int64_t ld_x, const void* r, int64_t ld_r, const void* w, int64_t rows,
                         int64_t cols, int32_t src, int32_t fmt, float eps, void* h, int64_t ld_h, void* y,

@@ -287,9 +287,9 @@ def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, fmt: int, eps: float = 1e
                      out: dict | None = None, stream=None) -> dict:
     """Root-mean-square norm of h = x + residual (fp32 or bf16 rows) times w,
     quantized row-wise to MX.  Returns q_row and s_row as ``quantize`` does, rstd
-    [rows] fp32, h where a residual is given, and y in x's type where ``want_y``
-    is set; ``out`` may supply any of them preallocated (h may be x or the
-    residual)."""
+    [rows] fp32 (NaN for rows of no columns), h where a residual is given, and y in
+    x's type where ``want_y`` is set; ``out`` may supply any of them preallocated (h
+    may be x or the residual)."""
     shape, dtype, device = x.shape, x.dtype, x.device
     if len(shape) != 2 or dtype not in _SRC or fmt not in BITS:
         raise ValueError("x must be a 2-D fp32/bf16 CUDA tensor, fmt a format")
@@ -313,6 +313,9 @@ def rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, fmt: int, eps: float = 1e
     _check(lib.mx_rmsnorm_quantize(px, ld_x, pr, ld_r, pw, rows, cols, _SRC[dtype], fmt, eps, ph, ld_h, py, ld_y,
                                    pq, ps, prstd, handle),
            "mx_rmsnorm_quantize")
+    if cols == 0 and rows > 0:  # the mean of nothing, which the library does not write
+        with torch.cuda.stream(stream):
+            o["rstd"].fill_(float("nan"))
     return o
 
 

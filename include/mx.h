@@ -218,7 +218,8 @@ int mx_gemm_mx(const void* a_q, const uint8_t* a_s, int32_t a_fmt, const void* b
  *   q_row, s_row  any format, row layout of mx_quantize.
  *   rstd    [rows] fp32, for mx_rmsnorm_backward; NULL: not written.
  * Pointers to rows, w and q_row 16-byte aligned, leading dimensions multiples of
- * 16 bytes.  Any rows < 2^31 and cols <= 2^24.  A row whose mean square is not
+ * 16 bytes and up to 2^40 elements (MX_ERR_UNSUPPORTED); those of a NULL matrix are not
+ * looked at.  Any rows < 2^31 and cols <= 2^24.  A row whose mean square is not
  * finite gives what the formulas give.  rows == 0 or cols == 0 writes nothing, rstd
  * (0 / 0 for a row of no columns) included.
  */
@@ -287,7 +288,7 @@ typedef struct {
  * mx_cache_write -- quantizes the keys and values of `tokens` tokens as mx_quantize
  * does (MX_RNE, blocks along dim) into the slots of a cache.
  *   k, v    [tokens][heads][dim] of type src: element (t, h, d) at t * ld + h * hs + d.
- *           16-byte aligned, ld and hs multiples of 16 bytes.
+ *           16-byte aligned, ld and hs multiples of 16 bytes, up to 2^40 elements.
  *   slots   [tokens] device array: token t goes to place slot % page of page
  *           slot / page.  A slot outside [0, pages * page) is not written.  Slots of
  *           one call are different.
@@ -317,8 +318,9 @@ int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t h
  * A query that sees no token gets o = 0 and lse = -inf.  What the cache holds
  * beyond a query's tokens, NaN included, does not reach it.  Scores, sums and
  * outputs are held in fp32; for the second product a weight is two bf16 terms, which
- * keep it to 2^-15.  B * heads and heads_q up to 65535, Lq * heads_q / heads up to 2^20 - 16,
- * max_len up to 2^30 (more: MX_ERR_UNSUPPORTED).
+ * keep it to 2^-15.  B * heads and heads_q up to 65535, Lq * heads_q / heads up to
+ * 2^20 - 16, max_len up to 2^30, ld_q, ld_table and ld_o up to 2^40 (more:
+ * MX_ERR_UNSUPPORTED).
  */
 int mx_attention(const mx_cache* cache, const void* q, int64_t ld_q, const int32_t* table, int64_t ld_table,
                  const int32_t* lens, int64_t B, int64_t Lq, int64_t heads_q, float scale, int64_t max_len,

@@ -16,14 +16,21 @@ bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0;
 int hip_status(hipError_t e) { return e == hipSuccess ? MX_OK : MX_ERR_HIP; }
 int64_t esz_of(int32_t src) { return src == MX_SRC_F32 ? 4 : 2; }
 
+// Elements between rows, heads or requests: no memory has them further apart, and their
+// bytes stay far below 2^63.
+constexpr int64_t kMaxPitch = (int64_t)1 << 40;
+
 // A row-major matrix that may be absent: its pitch covers a row, its rows start
 // on 16 bytes.
 int check_rows(const void* p, int64_t ld, int64_t cols, int64_t esz) {
   if (!p) return MX_OK;
   if (ld < cols) return MX_ERR_SHAPE;
+  if (ld > kMaxPitch) return MX_ERR_UNSUPPORTED;
   if (!aligned(p, 16) || (ld * esz) % 16) return MX_ERR_ALIGN;
   return MX_OK;
 }
+// Bytes between its rows; an absent matrix has none.
+int64_t pitch_of(const void* p, int64_t ld, int64_t esz) { return p ? ld * esz : 0; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 constexpr int64_t kMaxNormCols = (int64_t)1 << 24;
@@ -114,8 +121,8 @@ int mx_rmsnorm_quantize(const void* x, int64_t ld_x, const void* r, int64_t ld_r
   a.x = x;
   a.r = r;
   a.w = w;
-  a.ld_x = ld_x * esz;
-  a.ld_r = ld_r * esz;
+  a.ld_x = pitch_of(x, ld_x, esz);
+  a.ld_r = pitch_of(r, ld_r, esz);
   a.rows = rows;
   a.cols = cols;
   a.src = src;
@@ -123,8 +130,8 @@ int mx_rmsnorm_quantize(const void* x, int64_t ld_x, const void* r, int64_t ld_r
   a.eps = eps;
   a.h = h;
   a.y = y;
-  a.ld_h = ld_h * esz;
-  a.ld_y = ld_y * esz;
+  a.ld_h = pitch_of(h, ld_h, esz);
+  a.ld_y = pitch_of(y, ld_y, esz);
   a.q = (uint8_t*)q_row;
   a.s = s_row;
   a.rstd = rstd;
@@ -161,20 +168,24 @@ int mx_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld
       if (workspace_bytes < need) return MX_ERR_SHAPE;
     }
   }
+  if (rows == 0) {  // there are no rows, whatever their pitches are said to be
+    dy = h = dh = nullptr;
+    dx = nullptr;
+  }
   mx::NormGradArgs a;
   a.dy = dy;
   a.h = h;
   a.w = w;
   a.dh = dh;
   a.rstd = rstd;
-  a.ld_dy = ld_dy * esz;
-  a.ld_h = ld_h * esz;
-  a.ld_dh = ld_dh * esz;
+  a.ld_dy = pitch_of(dy, ld_dy, esz);
+  a.ld_h = pitch_of(h, ld_h, esz);
+  a.ld_dh = pitch_of(dh, ld_dh, esz);
   a.rows = rows;
   a.cols = cols;
   a.src = src;
   a.dx = dx;
-  a.ld_dx = ld_dx * esz;
+  a.ld_dx = pitch_of(dx, ld_dx, esz);
   a.dw = dw;
   a.partial = (float*)workspace;
   return hip_status(mx::launch_norm_grad(a, (hipStream_t)stream));
@@ -196,7 +207,8 @@ int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t h
   if (!src_ok(src) || tokens < 0 || ld_k < 0 || hs_k < 0 || ld_v < 0 || hs_v < 0) return MX_ERR_ARG;
   if (tokens == 0 || cache->heads == 0 || cache->pages == 0) return MX_OK;
   if (!k || !v || !slots) return MX_ERR_ARG;
-  if (tokens >= kMaxRows) return MX_ERR_UNSUPPORTED;
+  if (tokens >= kMaxRows || ld_k > kMaxPitch || hs_k > kMaxPitch || ld_v > kMaxPitch || hs_v > kMaxPitch)
+    return MX_ERR_UNSUPPORTED;
   const int64_t esz = esz_of(src);
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || (ld_k * esz) % 16 || (hs_k * esz) % 16 ||
       (ld_v * esz) % 16 || (hs_v * esz) % 16)
@@ -232,6 +244,7 @@ int mx_attention(const mx_cache* cache, const void* q, int64_t ld_q, const int32
   if (ld_table < 0 || (max_len + cache->page - 1) / cache->page > ld_table) return MX_ERR_SHAPE;
   if (B == 0 || Lq == 0 || heads_q == 0) return MX_OK;
   if (!q || !o || !lens || (max_len > 0 && !table)) return MX_ERR_ARG;
+  if (ld_q > kMaxPitch || ld_o > kMaxPitch || ld_table > kMaxPitch) return MX_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || (ld_q * 2) % 16 || !aligned(o, 2) || !aligned(lse, 4) || !aligned(table, 4) ||
       !aligned(lens, 4))
     return MX_ERR_ALIGN;

@@ -89,7 +89,7 @@ def step(layer: Layer, x: torch.Tensor, residual: torch.Tensor | None, cache: di
     h = n.get("h", x)
     qkv = product(n["y"], layer.wqkv, n).view(T, hq + 2 * hk, d)
     mx.cache_write(qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, cache, ACT)
-    a = mx.attention(qkv[:, :hq].unflatten(0, (B, T // B)), cache, ACT, table, lens)
+    a = mx.attention(qkv[:, :hq].unflatten(0, (B, T // max(B, 1))), cache, ACT, table, lens)
     x = product(a["o"].view(T, hq * d), layer.wo)
     n = mx.rmsnorm_quantize(x, layer.norm2, ACT, eps, residual=h, want_y=True)
     gate, up = product(n["y"], layer.wgu, n).chunk(2, dim=1)

@@ -310,7 +310,8 @@ int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t h
  *           included; clamped to [0, max_len].
  *   scale   factor of the scores (1 / sqrt(dim) as a rule).
  *   max_len host-known bound of lens, at most ld_table * page (MX_ERR_SHAPE).  The
- *           split of the work depends on it.
+ *           split of the work depends on it alone: where the table is wider than the
+ *           longest request, a bound near that length is faster.
  *   o       [B * Lq][heads_q][dim] bf16, ld_o elements between tokens.
  *   lse     [B * Lq][heads_q] fp32, log of the sum of exp(scores); may be NULL.
  *   workspace  mx_attention_workspace(...) bytes (may be 0), 16-byte aligned, in
@@ -318,7 +319,8 @@ int mx_cache_write(const mx_cache* cache, const void* k, int64_t ld_k, int64_t h
  * A query that sees no token gets o = 0 and lse = -inf.  What the cache holds
  * beyond a query's tokens, NaN included, does not reach it.  Scores, sums and
  * outputs are held in fp32; for the second product a weight is two bf16 terms, which
- * keep it to 2^-15.  B * heads and heads_q up to 65535, Lq * heads_q / heads up to
+ * keep it to 2^-15.  A cache element times its scale is taken as bf16, exactly from
+ * 2^-126 on.  B * heads and heads_q up to 65535, Lq * heads_q / heads up to
  * 2^20 - 16, max_len up to 2^30, ld_q, ld_table and ld_o up to 2^40 (more:
  * MX_ERR_UNSUPPORTED).
  */

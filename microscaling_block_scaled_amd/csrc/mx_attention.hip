@@ -71,8 +71,8 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift
 // ---------------------------------------------------------------------------
 // Rows of a key/value head are its (query token, query head) pairs.  Up to 16 of them:
 // a workgroup takes them all and one piece of the request's tokens, each wave 32
-// tokens at a time.  Both products run on 16x16x32 bf16 matrix instructions, to
-// which an element times its scale is exact:
+// tokens at a time.  Both products run on 16x16x32 bf16 matrix instructions, to which
+// an element times its scale is exact from bf16's smallest normal value, 2^-126, on:
 //   S^T = K Q^T   lane (l % 16, g = l / 16) takes dims g D/4 .. of token l % 16 and
 //                 feeds dims 8 j .. of them to instruction j, as the lane of Q does;
 //                 it gets its row's scores of tokens 4 g .. 4 g + 3
@@ -86,8 +86,10 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs p, int shift
 // its 32 tokens in whole 1 KB runs and reads them again from its own piece of LDS:
 // with loads in the operands' order (16 bytes of a token 32 bytes apart, scales byte
 // by byte) 32 requests to 16384 took 165 us, 136 us this way, and 140 us with weights of
-// two terms (661 MB: 4.7 TB/s).  The next 32
-// tokens are in flight meanwhile.
+// two terms (661 MB: 4.7 TB/s).  The next 32 tokens are in flight meanwhile.  What is
+// lost there: a CU holds a wave in 62 % of the time only (the large norm: 90 %).
+// Workgroups go to the eight XCDs by turns, so with 4 pieces piece p is always on XCDs
+// p and p + 4, and while every request has a first piece, few have a last one.
 constexpr int STEP = 32;  // tokens a wave takes at a time
 
 struct AttnArgs {
@@ -551,11 +553,13 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void k_attention(AttnArgs p) {
 //      (row_of), tokens in the order of the second product's lanes (8 g + 4 u + r for
 //      token 16 u + 4 g + r), and the four 16-byte pieces of a row exchanged by row, so
 //      that both the writes and the reads spread over the banks
-// Bound: the instructions of two workgroups a CU.  A step of a wave (32 tokens, 32 rows,
-// D = 128) is 32 matrix instructions of 16 cycles, 16 exponentials of 16 and about 180
-// others of 4, 1500 cycles in all, and takes 1500 to 1700; a workgroup's first loads take
-// 6000 and its outputs 2500 besides.  4 requests of 64 query tokens to 4096, 8 heads and
-// 32 query heads: 29 us and 7.1 us for the join; two prompts of up to 2048: 147 us.
+// Bound: by no unit, but by waves that wait and by CUs that stand empty.  4 requests of 64
+// query tokens to 4096, 8 heads and 32 query heads, D = 128, take 29 us and 7.4 us for
+// the join.  Of the 29 us the matrix units are busy for 13 %, vector instructions issue
+// for 22 %, and a CU holds a wave for 58 %: the pieces are cut by max_len, so shorter
+// requests have fewer, and a workgroup has 8 steps at most beside a beginning (length,
+// page, tokens: 6000 cycles) and an end (2500); the join reads 29 MB of partial sums
+// again.  Two prompts of up to 2048, 147 us: 16 %, 25 % and 55 %.
 // Tried without gain: all reads of a step ahead of their use, scores scaled in the
 // exponent's subtraction, the first tokens loaded before the request's length is known.
 template <int D>
@@ -976,17 +980,19 @@ struct Plan {
   int nr, waves, tiles, splits, chunk;
 };
 // Up to 16 rows the waves of a workgroup take tokens by turns; more rows are shared
-// out to them (8 requests to 4096, 8 heads of dim 128: 16 rows 21.6 us by tokens and
-// 22.1 by rows, 32 rows 29.4 and 24.0, 64 rows 35 and 27).  Workgroups are wanted
-// twice for each that the chip holds at a time (two of four waves a CU, one for dim
-// 256), which evens out requests of different lengths: 32 requests to 16384, dim 128,
-// took 136 us in 4 pieces, 143 in 16.  Few rows of up to 1024 tokens go to eight waves of
-// one workgroup, without pieces and a second launch, and so do more tokens where
-// requests and heads fill the chip by themselves.  Measured, 8 heads of dim 128 (us;
-// eight waves / pieces and their join): 1 request of 1000 10.6 / 10.0 and a launch
-// more, of 2048 16.3 / 10.0; 8 to 2048 17.1 / 13.0; 16 to 2048 17.1 / 20.2, to 4096
-// 28.4 / 28.1; 32 to 2048 19.6 / 27.6, to 8192 69 / 78, to 16384 135 / 142, but there
-// one long request among short ones would take twice as long.
+// out to them (8 requests to 4096, 8 heads of dim 128: 16 rows 22.4 us by tokens and
+// 23.7 by rows; two and four tiles of 16 rows by tokens, tried with weights of one term,
+// 29.4 and 35 instead of 24.0 and 27 by rows).  Workgroups are wanted twice for each
+// that the chip holds at a time (two of four waves a CU, one for dim 256): 32 requests
+// to 16384, dim 128, took 147 us in 4 pieces, 153 in 16 (with their join).  Few rows of up
+// to 1024 tokens go to eight waves of one workgroup, without pieces and a second launch,
+// and so do more tokens where requests and heads fill the chip by themselves.
+// Measured, 8 heads of dim 128 (us; eight waves / pieces and their join): 1 request of
+// 1000 11.3 / 10.1 and a launch more, of 2048 17.3 / 10.4; 8 to 2048 17.7 / 13.8; 16 to
+// 2048 18.7 / 20.8, to 4096 30.9 / 29.1; 32 to 2048 21.4 / 29.4, to 8192 72 / 81, to 16384
+// 140 / 147, but there one long request among short ones would take twice as long.
+// All of it goes by max_len, which the host knows, not by the lengths, which it does not: a
+// bound far above them leaves most pieces empty.
 Plan plan_of(int64_t B, int64_t Lq, int heads, int group, int dim, int64_t max_len) {
   Plan r;
   const int64_t rows = Lq * group;

@@ -17,9 +17,11 @@
 // of a quad hold one MX block and its maximum takes two DPP exchanges.  A row goes to
 // as many waves as give each lane one chunk (one for up to 512 elements, eight from
 // 2049 on), and to more chunks a lane only beyond 4096 elements.
-// Measured: 16384 x 4096 bf16 with a residual, 472 MB: 84.8 us (5.6 TB/s; a copy of
-// 1 GiB runs at 5.2); one row of 4096: 2.7 us.  The gradient of 8192 x 4096 with dh,
-// 268 MB: 45.9 us and 4.7 us for the sum of the partial sums.
+// Measured: 16384 x 4096 bf16 with a residual, 472 MB: 85 us (5.6 TB/s; a copy of
+// 1 GiB runs at 5.2); one row of 4096: 2.7 us.  8192 x 4096 with a residual (us; bf16 /
+// fp32): E4M3 42.7 / 84, E2M1 43.0 / 85, INT8 45 / 88, E2M3 and E3M2, whose stores are
+// of 4 and 2 bytes, 53 and 56 / 89 and 91.  The gradient of 8192 x 4096 with dh, 268 MB:
+// 45 us and 4.7 us for the sum of the partial sums; fp32, 537 MB: 97 us and 4.8.
 #include "mx_layer.h"
 #include "mx_rows.hpp"
 #include "mx_wave.hpp"

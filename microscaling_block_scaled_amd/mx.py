@@ -430,7 +430,8 @@ def attention(q: torch.Tensor, cache: dict, fmt: int, table: torch.Tensor, lens:
     dim]) over the requests' cached tokens: lens [B] int32 of them, the queries'
     own included, in the pages table [B, n] int32.  Query i sees the tokens before
     lens - Lq + i + 1.  Returns o like q and lse [B, Lq, query heads] fp32.
-    ``max_len``: a bound of lens (default: what the table holds); ``scale``:
+    ``max_len``: a bound of lens (default: what the table holds, which is slow where
+    that is far more than the longest request has, as the work is cut by it); ``scale``:
     default 1 / sqrt(dim); ``out`` and ``workspace`` may be supplied."""
     handle, dev = _on(stream, q)
     c = _cache(cache, fmt, dev)

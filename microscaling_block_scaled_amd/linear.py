@@ -49,11 +49,12 @@ def forward(x: torch.Tensor, w: torch.Tensor, r: Recipe, stream=None, qx: dict |
     in r.fmt (q_row, s_row), where its producer has quantized it."""
     T, H = x.shape
     O = w.shape[0]
-    if qx is None:
-        qx = mx.quantize(x, r.fmt, mx.LAYOUT_ROW, mx.RNE, stream=stream)
-    qw = mx.quantize(w, r.fmt, mx.LAYOUT_ROW | mx.LAYOUT_COLT, mx.RNE, stream=stream)
-    y = mx.gemm_bf16(qx["q_row"], qx["s_row"], r.fmt, qw["q_row"], qw["s_row"], r.fmt, T, O, H,
-                     stream=stream)
+    with torch.cuda.stream(stream):  # what the calls allocate, and free on return, is the stream's
+        if qx is None:
+            qx = mx.quantize(x, r.fmt, mx.LAYOUT_ROW, mx.RNE, stream=stream)
+        qw = mx.quantize(w, r.fmt, mx.LAYOUT_ROW | mx.LAYOUT_COLT, mx.RNE, stream=stream)
+        y = mx.gemm_bf16(qx["q_row"], qx["s_row"], r.fmt, qw["q_row"], qw["s_row"], r.fmt, T, O, H,
+                         stream=stream)
     return y, Saved(x, qw["q_colt"], qw["s_colt"])
 
 
@@ -61,16 +62,17 @@ def backward(dy: torch.Tensor, saved: Saved, r: Recipe, stream=None):
     """(dX as bf16, dW as fp32) for the upstream gradient dY [T x O]."""
     T, O = dy.shape
     H = saved.x.shape[1]
-    qdy = mx.quantize(dy, r.fmt, mx.LAYOUT_ROW, mx.SR, seed=r.seed, stream=stream)
-    dx = mx.gemm_bf16(qdy["q_row"], qdy["s_row"], r.fmt, saved.w_colt, saved.w_colt_s, r.fmt,
-                      T, H, O, stream=stream)
-    del qdy
-    qdyc = mx.quantize(dy, r.fmt, mx.LAYOUT_COLT, mx.SR, hadamard=True,
-                       hadamard_signs=r.hadamard_signs, seed=r.seed, stream=stream)
-    qxc = mx.quantize(saved.x, r.fmt, mx.LAYOUT_COLT, mx.RNE, hadamard=True,
-                      hadamard_signs=r.hadamard_signs, stream=stream)
-    dw = mx.gemm(qdyc["q_colt"], qdyc["s_colt"], r.fmt, qxc["q_colt"], qxc["s_colt"], r.fmt,
-                 O, H, T, stream=stream)
+    with torch.cuda.stream(stream):
+        qdy = mx.quantize(dy, r.fmt, mx.LAYOUT_ROW, mx.SR, seed=r.seed, stream=stream)
+        dx = mx.gemm_bf16(qdy["q_row"], qdy["s_row"], r.fmt, saved.w_colt, saved.w_colt_s, r.fmt,
+                          T, H, O, stream=stream)
+        del qdy
+        qdyc = mx.quantize(dy, r.fmt, mx.LAYOUT_COLT, mx.SR, hadamard=True,
+                           hadamard_signs=r.hadamard_signs, seed=r.seed, stream=stream)
+        qxc = mx.quantize(saved.x, r.fmt, mx.LAYOUT_COLT, mx.RNE, hadamard=True,
+                          hadamard_signs=r.hadamard_signs, stream=stream)
+        dw = mx.gemm(qdyc["q_colt"], qdyc["s_colt"], r.fmt, qxc["q_colt"], qxc["s_colt"], r.fmt,
+                     O, H, T, stream=stream)
     return dx, dw
 
 
